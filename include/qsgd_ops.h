@@ -1,0 +1,122 @@
+/*
+ * qsgd_ops.h -- C ABI of the low-precision training operators of libqsgd.so:
+ * an 8-bit linear layer (quantizer, product, layer, gradient) and distillation
+ * from a teacher's top logits. They stand before the compressor of qsgd.h in a
+ * data-parallel step: the layer's weight gradient (fp32, row-major) is what
+ * qsgd_encode takes.
+ *
+ * The quantizer is the compressor's max-norm scale (QSGD_NORM_MAX) with s = 127
+ * levels and one bucket per row (or column), rounded to the nearest level:
+ *   y      = x, or RN32(x fold) with one factor per position of the reduced axis;
+ *   scale  = RN32(max |y| / 127);
+ *   level  = RNE(RN32(y / scale)) held to [-127, 127]; every level of a row is 0
+ *            where its scale is 0 or not finite. A row that holds an infinity or a
+ *            NaN has that as its scale, so its products are NaN.
+ *
+ * Conventions are those of qsgd.h: device pointers owned by the caller, work
+ * enqueued on `stream` without synchronizing, argument errors found on the host
+ * before anything is enqueued (QSGD_ERR_INVALID_ARG), no device memory allocated,
+ * no state kept between calls. Matrices are row-major with a row stride (ld...,
+ * in elements) of at least the row length; pointers need the alignment of
+ * their elements only (16-byte aligned pointers and strides take faster
+ * loads). Workspaces (16-byte aligned) hold unspecified values afterwards and are
+ * NULL where the size function gives 0. Results do not depend on what the
+ * workspace held, and are the same on every run. Rows and columns are below
+ * 2^31 each; a call with no rows or no columns to write enqueues nothing.
+ */
+#ifndef QSGD_OPS_H
+#define QSGD_OPS_H
+
+#include "qsgd.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+typedef enum { QSGD_F32 = 0, QSGD_F16 = 1, QSGD_BF16 = 2, QSGD_I32 = 3, QSGD_I64 = 4 } qsgd_dtype;
+
+/*
+ * qsgd_int8_quantize: levels and scale of each row.
+ *   x       [rows, cols] of `dtype` (QSGD_F32, QSGD_F16 or QSGD_BF16), row stride ldx.
+ *   fold    [cols] fp32 or NULL: y = RN32(x[r, c] fold[c]).
+ *   levels  [rows, cols] int8 output, row stride ldl.
+ *   scale   [rows] fp32 output (0 where cols == 0).
+ */
+qsgd_status qsgd_int8_quantize(const void *x, qsgd_dtype dtype, uint64_t rows, uint64_t cols, uint64_t ldx,
+                               const float *fold, int8_t *levels, uint64_t ldl, float *scale,
+                               hipStream_t stream);
+
+/*
+ * qsgd_int8_quantize_transposed: levels and scale of each column, the levels
+ * written transposed.
+ *   fold    [rows] fp32 or NULL: y = RN32(x[r, c] fold[r]).
+ *   levels  [cols, rows] int8 output, row stride ldl >= rows.
+ *   scale   [cols] fp32 output (0 where rows == 0).
+ *   workspace  qsgd_int8_quantize_transposed_workspace(rows, cols) bytes.
+ */
+uint64_t qsgd_int8_quantize_transposed_workspace(uint64_t rows, uint64_t cols);
+qsgd_status qsgd_int8_quantize_transposed(const void *x, qsgd_dtype dtype, uint64_t rows, uint64_t cols,
+                                          uint64_t ldx, const float *fold, int8_t *levels, uint64_t ldl,
+                                          float *scale, void *workspace, hipStream_t stream);
+
+/*
+ * qsgd_int8_matmul: y[i, j] = RN(RN32(RN32(RN32(acc) sa[i]) sb[j]) + bias[j]) with
+ * acc = sum_p a[i, p] b[j, p], exact for every k below 2^31.
+ *   a     [m, k] int8, row stride lda; sa [m] fp32 (a token's scale).
+ *   b     [n, k] int8, row stride ldb; sb [n] fp32 (a channel's scale) or NULL (1).
+ *   bias  [n] fp32 or NULL.
+ *   y     [m, n] of `dtype` (QSGD_F32, QSGD_F16 or QSGD_BF16), row stride ldy.
+ *   workspace  qsgd_int8_matmul_workspace(...) bytes, a function of the sizes,
+ *         the strides and the pointers' alignment to 16 bytes alone.
+ * Levels of -128 are taken as they are. k == 0 gives the bias (or 0).
+ */
+uint64_t qsgd_int8_matmul_workspace(const int8_t *a, uint64_t lda, const int8_t *b, uint64_t ldb, uint64_t m,
+                                    uint64_t n, uint64_t k);
+qsgd_status qsgd_int8_matmul(const int8_t *a, uint64_t lda, const float *sa, const int8_t *b, uint64_t ldb,
+                             const float *sb, const float *bias, void *y, qsgd_dtype dtype, uint64_t ldy,
+                             uint64_t m, uint64_t n, uint64_t k, void *workspace, hipStream_t stream);
+
+/*
+ * qsgd_int8_linear: the layer. Quantizes the rows of x and multiplies:
+ * y = qsgd_int8_matmul(levels and scale of x, w, sw, bias), in x's type.
+ *   x   [m, k] of `dtype`, row stride ldx.
+ *   w   [n, k] int8 levels of the weight, row stride ldw; sw [n] fp32.
+ *   xq  [m, ldxq] int8 and sx [m] fp32 outputs: the levels (columns past k up to
+ *       a multiple of 16 are set to 0) and scales of x, which the gradient takes.
+ *       ldxq is at least k rounded up to a multiple of 16, and a multiple of 16; xq
+ *       is 16-byte aligned. Both may be NULL (ldxq 0) where no gradient follows;
+ *       the workspace then holds them.
+ *   workspace  qsgd_int8_linear_workspace(...) bytes; `keep` nonzero: xq and sx are
+ *       the caller's.
+ */
+uint64_t qsgd_int8_linear_workspace(const int8_t *w, uint64_t ldw, uint64_t m, uint64_t n, uint64_t k, int keep);
+qsgd_status qsgd_int8_linear(const void *x, qsgd_dtype dtype, uint64_t ldx, const int8_t *w, uint64_t ldw,
+                             const float *sw, const float *bias, void *y, uint64_t ldy, int8_t *xq,
+                             uint64_t ldxq, float *sx, uint64_t m, uint64_t n, uint64_t k, void *workspace,
+                             hipStream_t stream);
+
+/*
+ * qsgd_int8_linear_backward: the gradient of y = (sx xq) (sw w)^T with respect to
+ * the two factors (straight through the rounding that made them), with gy itself
+ * held in 8 bits. The scales of the summed axis are folded into gy before it is
+ * quantized, so both sums run over integers with w and xq as they are:
+ *   gq, sg = rows of gy quantized with fold = sw;     gx[i, p] = RN(sg[i] sum_j gq[i, j] w[j, p])
+ *   hq, sh = columns of gy quantized with fold = sx;  gw[j, p] = RN32(sh[j] sum_i hq[i, j] xq[i, p])
+ * Each entry of gx is within sum_j |w[j, p]| sg[i] / 2 of the product in reals
+ * (up to fp32 rounding), and of gw within sum_i |xq[i, p]| sh[j] / 2.
+ *   gy  [m, n] of `dtype`, row stride ldgy.
+ *   xq  [m, k] int8, row stride ldxq, sx [m], w [n, k], sw [n]: as in the layer.
+ *   gx  [m, k] of `dtype`, row stride ldgx, or NULL (not computed).
+ *   gw  [n, k] fp32, row stride ldgw, or NULL (not computed).
+ *   workspace  qsgd_int8_linear_backward_workspace(m, n, k) bytes.
+ */
+uint64_t qsgd_int8_linear_backward_workspace(uint64_t m, uint64_t n, uint64_t k);
+qsgd_status qsgd_int8_linear_backward(const void *gy, qsgd_dtype dtype, uint64_t ldgy, const int8_t *xq,
+                                      uint64_t ldxq, const float *sx, const int8_t *w, uint64_t ldw,
+                                      const float *sw, void *gx, uint64_t ldgx, float *gw, uint64_t ldgw,
+                                      uint64_t m, uint64_t n, uint64_t k, void *workspace, hipStream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+#endif /* QSGD_OPS_H */

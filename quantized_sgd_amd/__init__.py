@@ -20,7 +20,7 @@ __all__ = [
     "decode", "RaggedLayout", "quantize_ragged", "encode_ragged", "decode_ragged",
     "max_bucket", "max_streams", "decode_accumulate", "decode_accumulate_ragged", "OMEGA", "GAMMA",
     "L2", "MAXNORM", "encode_noalloc", "encode_noalloc_capacity_words", "quantize_seglen", "encode_seglen",
-    "decode_seglen",
+    "decode_seglen", "int8_quantize", "int8_matmul", "int8_linear", "int8_linear_backward",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -438,3 +438,6 @@ def decode_seglen(words: torch.Tensor, offsets: torch.Tensor, seg_len, s: int, d
                                     sl.ctypes.data, len(sl), s, d, _dev(v_hat, torch.float32, "v_hat"),
                                     _stream(stream)), "qsgd_decode_seglen")
     return v_hat[:n]
+
+
+from .int8 import int8_linear, int8_linear_backward, int8_matmul, int8_quantize  # noqa: E402

@@ -1,0 +1,100 @@
+"""Marshalling shared by the operator bindings (int8.py, distill.py): argument
+checks, streams, buffers. The C ABI is include/qsgd_ops.h."""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+
+import torch
+
+from . import QsgdError, lib
+
+DTYPE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2, torch.int32: 3, torch.int64: 4}
+FLOATS = (torch.float32, torch.float16, torch.bfloat16)
+
+u64 = ctypes.c_uint64
+vp = ctypes.c_void_p
+
+_bound = {}
+
+
+def function(name: str, restype, *argtypes):
+    """The library's function with its C types, looked up once."""
+    f = _bound.get(name)
+    if f is None:
+        f = getattr(lib(), name)
+        f.argtypes = argtypes
+        f.restype = restype
+        _bound[name] = f
+    return f
+
+
+def check(status: int, what: str):
+    if status:
+        raise QsgdError(status, what)
+
+
+def matrix(t: torch.Tensor, name: str, dtypes, rows=None, cols=None):
+    """A 2-D device tensor of one of `dtypes` (and of the given sizes) whose rows
+    are contiguous and do not overlap. Returns its row stride."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, got {t.dim()}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be one of {', '.join(map(str, dtypes))}, got {t.dtype}")
+    r, c = t.shape
+    if (rows is not None and r != rows) or (cols is not None and c != cols):
+        raise ValueError(f"{name} must be [{'any' if rows is None else rows}, {'any' if cols is None else cols}], "
+                         f"got [{r}, {c}]")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    ld, step = t.stride()
+    if c > 1 and step != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if r <= 1 or c == 0:
+        return max(c, 1)
+    if ld < c:
+        raise ValueError(f"{name} must have rows that do not overlap")
+    return ld
+
+
+def vector(t, name: str, n: int, device, dtype=torch.float32):
+    """The address of a contiguous device vector of n values, or None."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 1 or t.shape[0] != n:
+        raise ValueError(f"{name} must be [{n}], got {list(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    if n > 1 and t.stride(0) != 1:
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def same_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} must be on {device}, is on {t.device}")
+
+
+_nothing = contextlib.nullcontext()
+
+
+def on(device, stream):
+    """The context in which a call allocates and launches: the tensors' device
+    and, where one is given, the stream (so that buffers made here belong to
+    it)."""
+    if stream is not None:
+        return torch.cuda.stream(stream)
+    if device.index == torch.cuda.current_device():
+        return _nothing
+    return torch.cuda.device(device)
+
+
+def raw_stream(device) -> int:
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def scratch(nbytes: int, device):
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None

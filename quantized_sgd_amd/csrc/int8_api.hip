@@ -1,0 +1,346 @@
+// Host side of the 8-bit linear layer (include/qsgd_ops.h): argument checks,
+// choice of kernels, workspace layout, launches.
+#include "qsgd_ops.h"
+
+#include <algorithm>
+
+#include "int8_matmul.h"
+#include "int8_quantize.h"
+
+using namespace qsgd::ops;
+
+namespace {
+
+// ---- quantizer ----
+
+// Rows of up to 2048 values are a wave's, longer ones a workgroup's; beyond 16384
+// they are read twice.
+template <class T>
+void launch_rows(const QuantizeParams &p, hipStream_t stream) {
+    const dim3 by_wave = grid_of(div_up(p.rows, 4)), by_group = grid_of(p.rows);
+    const uint32_t n = p.wide;
+    if (n <= 512) quantize_rows_kernel<T, 64, 1><<<by_wave, 256, 0, stream>>>(p);
+    else if (n <= 1024) quantize_rows_kernel<T, 64, 2><<<by_wave, 256, 0, stream>>>(p);
+    else if (n <= 2048) quantize_rows_kernel<T, 256, 1><<<by_group, 256, 0, stream>>>(p);
+    else if (n <= 4096) quantize_rows_kernel<T, 256, 2><<<by_group, 256, 0, stream>>>(p);
+    else if (n <= 8192) quantize_rows_kernel<T, 256, 4><<<by_group, 256, 0, stream>>>(p);
+    else if (n <= 16384) quantize_rows_kernel<T, 256, 8><<<by_group, 256, 0, stream>>>(p);
+    else quantize_rows_kernel<T, 256, 0><<<by_group, 256, 0, stream>>>(p);
+}
+
+qsgd_status quantize_rows(const void *x, qsgd_dtype dtype, uint64_t rows, uint64_t cols, uint64_t ldx,
+                          const float *fold, int8_t *levels, uint64_t ldl, float *scale, uint64_t wide,
+                          hipStream_t stream) {
+    if (rows == 0) return QSGD_OK;
+    return with_type(dtype, [&](auto t) {
+        launch_rows<decltype(t)>({x, fold, levels, scale, ldx, ldl, (uint32_t)rows, (uint32_t)cols, (uint32_t)wide},
+                                 stream);
+        return launched();
+    });
+}
+
+// Runs of rows for the column maxima: enough workgroups for the chip, at least 64
+// rows each.
+uint32_t column_splits(uint64_t rows, uint64_t cols) {
+    const uint64_t blocks = div_up(cols, 512);
+    return (uint32_t)std::max<uint64_t>(1, std::min({(uint64_t)kMaxSplits, div_up(1024, blocks), div_up(rows, 64)}));
+}
+
+qsgd_status quantize_columns(const void *x, qsgd_dtype dtype, uint64_t rows, uint64_t cols, uint64_t ldx,
+                             const float *fold, int8_t *levels, uint64_t ldl, float *scale, uint64_t wide,
+                             void *workspace, hipStream_t stream) {
+    if (cols == 0) return QSGD_OK;
+    const uint32_t splits = column_splits(rows, cols);
+    const uint32_t tr = (uint32_t)std::max<uint64_t>(1, div_up(wide, 128)), tc = (uint32_t)div_up(cols, 64);
+    return with_type(dtype, [&](auto t) {
+        using T = decltype(t);
+        const TransposeParams p{x, fold, levels, scale, (uint32_t *)workspace, ldx, ldl, (uint32_t)rows, (uint32_t)cols,
+                                (uint32_t)wide, splits, (uint32_t)div_up(rows, splits), tr, tc};
+        column_max_kernel<T><<<dim3((uint32_t)div_up(cols, 512), splits), 256, 0, stream>>>(p);
+        transpose_kernel<T><<<grid_of((uint64_t)tr * tc), 256, 0, stream>>>(p);
+        return launched();
+    });
+}
+
+qsgd_status transpose_bytes(const int8_t *x, uint64_t rows, uint64_t cols, uint64_t ldx, int8_t *out, uint64_t ldo,
+                            uint64_t wide, hipStream_t stream) {
+    if (cols == 0 || wide == 0) return QSGD_OK;
+    const uint32_t tr = (uint32_t)div_up(wide, 128), tc = (uint32_t)div_up(cols, 64);
+    const TransposeParams p{x, nullptr, out, nullptr, nullptr, ldx, ldo, (uint32_t)rows, (uint32_t)cols, (uint32_t)wide,
+                            0, 0, tr, tc};
+    transpose_kernel<int8_t><<<grid_of((uint64_t)tr * tc), 256, 0, stream>>>(p);
+    return launched();
+}
+
+// ---- product ----
+
+using Tile256 = Tile<2, 2, 8, 8, 4>;
+using Tile128 = Tile<2, 2, 4, 4, 4>;
+using Tile64 = Tile<2, 2, 2, 2, 4>;
+
+constexpr uint64_t kMaxK = 1u << 23;  // a tile's row offsets are 32-bit
+constexpr uint64_t kSafeSteps = 2047; // 64-byte steps whose sum of products stays below 2^31 (2047 * 64 * 128^2)
+constexpr uint64_t kCus = 256;
+
+struct Plan {
+    bool skinny = false;
+    bool repack_a = false, repack_b = false;
+    int tile = 0;
+    uint64_t tiles_m = 0, tiles_n = 0, splits = 1, steps = 0;
+    uint64_t lda = 0, ldb = 0;
+    uint64_t at_a = 0, at_b = 0, at_part = 0, bytes = 0;  // workspace
+};
+
+// `padded`: the bytes of a row past k up to a multiple of 16 are zeros.
+bool loads_as_is(bool aligned, uint64_t ld, uint64_t k, bool padded) {
+    return aligned && ld % 16 == 0 && ld <= kMaxK && (k % 16 == 0 || padded);
+}
+
+Plan plan_matmul(bool a_aligned, uint64_t lda, bool a_padded, bool b_aligned, uint64_t ldb, bool b_padded, uint64_t m,
+                 uint64_t n, uint64_t k) {
+    Plan p;
+    p.lda = lda;
+    p.ldb = ldb;
+    const uint64_t all = std::max<uint64_t>(1, div_up(k, 64));
+    if (m <= 32 && n <= (1u << 24) && all <= kSafeSteps) {
+        p.skinny = true;
+        return p;
+    }
+    const uint64_t kp = round_up(std::max<uint64_t>(k, 1), 64);
+    if (!loads_as_is(a_aligned, lda, k, a_padded)) {
+        p.repack_a = true;
+        p.lda = kp;
+        p.at_a = p.bytes;
+        p.bytes += round_up(m * kp, 256);
+    }
+    if (!loads_as_is(b_aligned, ldb, k, b_padded)) {
+        p.repack_b = true;
+        p.ldb = kp;
+        p.at_b = p.bytes;
+        p.bytes += round_up(n * kp, 256);
+    }
+    const uint64_t side[3] = {64, 128, 256};
+    p.tile = 2;
+    while (p.tile > 0 && div_up(m, side[p.tile]) * div_up(n, side[p.tile]) < kCus * 3 / 4) --p.tile;
+    p.tiles_m = div_up(m, side[p.tile]);
+    p.tiles_n = div_up(n, side[p.tile]);
+    const uint64_t tiles = p.tiles_m * p.tiles_n;
+    uint64_t splits = div_up(all, kSafeSteps);
+    if (tiles < kCus) splits = std::max(splits, std::min({kCus / tiles, all / 8, (uint64_t)16}));
+    p.steps = div_up(all, splits);
+    p.splits = div_up(all, p.steps);
+    if (p.splits > 1) {
+        p.at_part = p.bytes;
+        p.bytes += round_up(p.splits * m * n * 4, 256);
+    }
+    return p;
+}
+
+template <class C, class OUT>
+void launch_tiles(const MatmulParams &p, hipStream_t stream) {
+    matmul_kernel<C, OUT><<<dim3(p.tiles_m * p.tiles_n, p.splits), C::NW * 64, 0, stream>>>(p);
+}
+
+template <class OUT>
+void launch_matmul(const Plan &plan, const MatmulParams &p, hipStream_t stream) {
+    if (plan.tile == 2) launch_tiles<Tile256, OUT>(p, stream);
+    else if (plan.tile == 1) launch_tiles<Tile128, OUT>(p, stream);
+    else launch_tiles<Tile64, OUT>(p, stream);
+}
+
+qsgd_status repack(const int8_t *src, uint64_t lds, int8_t *dst, uint64_t ldd, uint64_t rows, uint64_t cols,
+                   hipStream_t stream) {
+    const RepackParams r{src, dst, lds, ldd, (uint32_t)rows, (uint32_t)cols};
+    repack_kernel<<<grid_of(div_up(rows * (ldd / 16), 256)), 256, 0, stream>>>(r);
+    return launched();
+}
+
+qsgd_status run_matmul(const Plan &plan, const int8_t *a, const float *sa, const int8_t *b, const float *sb,
+                       const float *bias, void *y, qsgd_dtype dtype, uint64_t ldy, uint64_t lda, uint64_t ldb,
+                       uint64_t m, uint64_t n, uint64_t k, void *workspace, hipStream_t stream) {
+    if (m == 0 || n == 0) return QSGD_OK;
+    char *ws = (char *)workspace;
+    MatmulParams p{a, b, sa, sb, bias, y, nullptr, plan.lda, plan.ldb, ldy, (uint32_t)m, (uint32_t)n, (uint32_t)k,
+                   (uint32_t)plan.tiles_m, (uint32_t)plan.tiles_n, (uint32_t)plan.splits, (uint32_t)plan.steps};
+    if (plan.repack_a) {
+        p.a = (const int8_t *)(ws + plan.at_a);
+        const qsgd_status st = repack(a, lda, (int8_t *)(ws + plan.at_a), plan.lda, m, k, stream);
+        if (st != QSGD_OK) return st;
+    }
+    if (plan.repack_b) {
+        p.b = (const int8_t *)(ws + plan.at_b);
+        const qsgd_status st = repack(b, ldb, (int8_t *)(ws + plan.at_b), plan.ldb, n, k, stream);
+        if (st != QSGD_OK) return st;
+    }
+    return with_type(dtype, [&](auto t) {
+        using OUT = decltype(t);
+        if (plan.skinny) {
+            const dim3 grid((uint32_t)div_up(n, 16));
+            if (m <= 16) skinny_kernel<1, 1, OUT><<<grid, 512, 0, stream>>>(p);
+            else skinny_kernel<2, 1, OUT><<<grid, 512, 0, stream>>>(p);
+        } else if (plan.splits == 1) {
+            launch_matmul<OUT>(plan, p, stream);
+        } else {
+            p.part = (int32_t *)(ws + plan.at_part);
+            launch_matmul<float>(plan, p, stream);
+            join_kernel<OUT><<<grid_of(div_up(m * n, 1024)), 256, 0, stream>>>(p);
+        }
+        return launched();
+    });
+}
+
+Plan plan_of(const int8_t *a, uint64_t lda, bool a_padded, const int8_t *b, uint64_t ldb, uint64_t m, uint64_t n,
+             uint64_t k) {
+    return plan_matmul(aligned_to(a, 16), lda, a_padded, aligned_to(b, 16), ldb, false, m, n, k);
+}
+
+bool dims_ok(uint64_t m, uint64_t n, uint64_t k) { return m <= kMaxDim && n <= kMaxDim && k <= kMaxDim; }
+
+uint64_t padded16(uint64_t k) { return round_up(k, 16); }
+
+// Workspace of the gradient: the two quantized forms of gy, w and xq transposed,
+// the larger of the two products' own.
+struct BackwardPlan {
+    uint64_t ldn, ldm;  // rows of gq and w^T, rows of hq and xq^T
+    uint64_t gq, sg, wt, hq, sh, xt, cols, own, bytes;
+    Plan gx, gw;
+};
+
+BackwardPlan plan_backward(uint64_t m, uint64_t n, uint64_t k) {
+    BackwardPlan b;
+    b.ldn = padded16(n);
+    b.ldm = padded16(m);
+    b.gx = plan_matmul(true, b.ldn, true, true, b.ldn, true, m, k, n);
+    b.gw = plan_matmul(true, b.ldm, true, true, b.ldm, true, n, k, m);
+    uint64_t at = 0;
+    const auto take = [&](uint64_t bytes) {
+        const uint64_t here = at;
+        at += round_up(bytes, 256);
+        return here;
+    };
+    b.gq = take(m * b.ldn);
+    b.sg = take(4 * m);
+    b.wt = take(k * b.ldn);
+    b.hq = take(n * b.ldm);
+    b.sh = take(4 * n);
+    b.xt = take(k * b.ldm);
+    b.cols = take(qsgd_int8_quantize_transposed_workspace(m, n));
+    b.own = take(std::max(b.gx.bytes, b.gw.bytes));
+    b.bytes = at;
+    return b;
+}
+
+}  // namespace
+
+extern "C" {
+
+qsgd_status qsgd_int8_quantize(const void *x, qsgd_dtype dtype, uint64_t rows, uint64_t cols, uint64_t ldx,
+                               const float *fold, int8_t *levels, uint64_t ldl, float *scale, hipStream_t stream) {
+    if (!is_float(dtype) || !dims_ok(rows, cols, 0) || ldx < cols || ldl < cols) return QSGD_ERR_INVALID_ARG;
+    if (rows == 0) return QSGD_OK;
+    if (!scale || (cols && (!x || !levels))) return QSGD_ERR_INVALID_ARG;
+    return quantize_rows(x, dtype, rows, cols, ldx, fold, levels, ldl, scale, cols, stream);
+}
+
+uint64_t qsgd_int8_quantize_transposed_workspace(uint64_t rows, uint64_t cols) {
+    if (!dims_ok(rows, cols, 0) || cols == 0) return 0;
+    return round_up(4 * cols * column_splits(rows, cols), 256);
+}
+
+qsgd_status qsgd_int8_quantize_transposed(const void *x, qsgd_dtype dtype, uint64_t rows, uint64_t cols, uint64_t ldx,
+                                          const float *fold, int8_t *levels, uint64_t ldl, float *scale,
+                                          void *workspace, hipStream_t stream) {
+    if (!is_float(dtype) || !dims_ok(rows, cols, 0) || ldx < cols || ldl < rows) return QSGD_ERR_INVALID_ARG;
+    if (cols == 0) return QSGD_OK;
+    if (!scale || !workspace || !aligned_to(workspace, 16) || (rows && (!x || !levels))) return QSGD_ERR_INVALID_ARG;
+    return quantize_columns(x, dtype, rows, cols, ldx, fold, levels, ldl, scale, rows, workspace, stream);
+}
+
+uint64_t qsgd_int8_matmul_workspace(const int8_t *a, uint64_t lda, const int8_t *b, uint64_t ldb, uint64_t m,
+                                    uint64_t n, uint64_t k) {
+    if (!dims_ok(m, n, k) || k > kMaxK || m == 0 || n == 0) return 0;
+    return plan_of(a, lda, false, b, ldb, m, n, k).bytes;
+}
+
+qsgd_status qsgd_int8_matmul(const int8_t *a, uint64_t lda, const float *sa, const int8_t *b, uint64_t ldb,
+                             const float *sb, const float *bias, void *y, qsgd_dtype dtype, uint64_t ldy, uint64_t m,
+                             uint64_t n, uint64_t k, void *workspace, hipStream_t stream) {
+    if (!is_float(dtype) || !dims_ok(m, n, k) || lda < k || ldb < k || ldy < n) return QSGD_ERR_INVALID_ARG;
+    if (m == 0 || n == 0) return QSGD_OK;
+    if (k > kMaxK) return QSGD_ERR_UNSUPPORTED;
+    if (!sa || !y || (k && (!a || !b))) return QSGD_ERR_INVALID_ARG;
+    const Plan plan = plan_of(a, lda, false, b, ldb, m, n, k);
+    if (plan.bytes && (!workspace || !aligned_to(workspace, 16))) return QSGD_ERR_INVALID_ARG;
+    return run_matmul(plan, a, sa, b, sb, bias, y, dtype, ldy, lda, ldb, m, n, k, workspace, stream);
+}
+
+uint64_t qsgd_int8_linear_workspace(const int8_t *w, uint64_t ldw, uint64_t m, uint64_t n, uint64_t k, int keep) {
+    if (!dims_ok(m, n, k) || k > kMaxK || m == 0) return 0;
+    const uint64_t ldq = padded16(k);
+    uint64_t bytes = n == 0 ? 0 : plan_of(nullptr, ldq, true, w, ldw, m, n, k).bytes;
+    if (!keep) bytes += round_up(m * ldq, 256) + round_up(4 * m, 256);
+    return bytes;
+}
+
+qsgd_status qsgd_int8_linear(const void *x, qsgd_dtype dtype, uint64_t ldx, const int8_t *w, uint64_t ldw,
+                             const float *sw, const float *bias, void *y, uint64_t ldy, int8_t *xq, uint64_t ldxq,
+                             float *sx, uint64_t m, uint64_t n, uint64_t k, void *workspace, hipStream_t stream) {
+    if (!is_float(dtype) || !dims_ok(m, n, k) || ldx < k || ldw < k || ldy < n) return QSGD_ERR_INVALID_ARG;
+    if (m == 0) return QSGD_OK;
+    if (k > kMaxK) return QSGD_ERR_UNSUPPORTED;
+    if ((xq == nullptr) != (sx == nullptr)) return QSGD_ERR_INVALID_ARG;
+    if (xq && (ldxq < padded16(k) || ldxq % 16 || ldxq > kMaxK || !aligned_to(xq, 16))) return QSGD_ERR_INVALID_ARG;
+    if ((k && !x) || (n && (!sw || !y || (k && !w)))) return QSGD_ERR_INVALID_ARG;
+    const uint64_t need = qsgd_int8_linear_workspace(w, ldw, m, n, k, xq != nullptr);
+    if (need && (!workspace || !aligned_to(workspace, 16))) return QSGD_ERR_INVALID_ARG;
+    const uint64_t ldq = xq ? ldxq : padded16(k);
+    const Plan plan = n ? plan_of(nullptr, ldq, true, w, ldw, m, n, k) : Plan{};
+    if (!xq) {
+        xq = (int8_t *)workspace + plan.bytes;
+        sx = (float *)((char *)workspace + plan.bytes + round_up(m * ldq, 256));
+    }
+    const qsgd_status st = quantize_rows(x, dtype, m, k, ldx, nullptr, xq, ldq, sx, padded16(k), stream);
+    if (st != QSGD_OK || n == 0) return st;
+    return run_matmul(plan, xq, sx, w, sw, bias, y, dtype, ldy, ldq, ldw, m, n, k, workspace, stream);
+}
+
+uint64_t qsgd_int8_linear_backward_workspace(uint64_t m, uint64_t n, uint64_t k) {
+    if (!dims_ok(m, n, k) || m > kMaxK || n > kMaxK) return 0;
+    return plan_backward(m, n, k).bytes;
+}
+
+qsgd_status qsgd_int8_linear_backward(const void *gy, qsgd_dtype dtype, uint64_t ldgy, const int8_t *xq, uint64_t ldxq,
+                                      const float *sx, const int8_t *w, uint64_t ldw, const float *sw, void *gx,
+                                      uint64_t ldgx, float *gw, uint64_t ldgw, uint64_t m, uint64_t n, uint64_t k,
+                                      void *workspace, hipStream_t stream) {
+    if (!is_float(dtype) || !dims_ok(m, n, k) || ldgy < n || (gx && (ldgx < k || ldw < k)) ||
+        (gw && (ldgw < k || ldxq < k)))
+        return QSGD_ERR_INVALID_ARG;
+    if (k == 0 || (!gx && !gw)) return QSGD_OK;
+    if (m > kMaxK || n > kMaxK) return QSGD_ERR_UNSUPPORTED;
+    if (m && n && (!gy || (gx && (!w || !sw)) || (gw && (!xq || !sx)))) return QSGD_ERR_INVALID_ARG;
+    const BackwardPlan b = plan_backward(m, n, k);
+    if (b.bytes && (!workspace || !aligned_to(workspace, 16))) return QSGD_ERR_INVALID_ARG;
+    char *ws = (char *)workspace;
+    qsgd_status st = QSGD_OK;
+    if (gx) {
+        int8_t *gq = (int8_t *)(ws + b.gq), *wt = (int8_t *)(ws + b.wt);
+        float *sg = (float *)(ws + b.sg);
+        st = quantize_rows(gy, dtype, m, n, ldgy, sw, gq, b.ldn, sg, b.ldn, stream);
+        if (st == QSGD_OK) st = transpose_bytes(w, n, k, ldw, wt, b.ldn, b.ldn, stream);
+        if (st == QSGD_OK)
+            st = run_matmul(b.gx, gq, sg, wt, nullptr, nullptr, gx, dtype, ldgx, b.ldn, b.ldn, m, k, n, ws + b.own, stream);
+        if (st != QSGD_OK) return st;
+    }
+    if (gw) {
+        int8_t *hq = (int8_t *)(ws + b.hq), *xt = (int8_t *)(ws + b.xt);
+        float *sh = (float *)(ws + b.sh);
+        st = quantize_columns(gy, dtype, m, n, ldgy, sx, hq, b.ldm, sh, b.ldm, ws + b.cols, stream);
+        if (st == QSGD_OK) st = transpose_bytes(xq, m, k, ldxq, xt, b.ldm, b.ldm, stream);
+        if (st == QSGD_OK)
+            st = run_matmul(b.gw, hq, sh, xt, nullptr, nullptr, gw, QSGD_F32, ldgw, b.ldm, b.ldm, n, k, m, ws + b.own, stream);
+    }
+    return st;
+}
+
+}  // extern "C"

@@ -1,0 +1,97 @@
+// Shared pieces of the low-precision training operators (include/qsgd_ops.h):
+// element types, loads and stores of eight elements at any element alignment,
+// wave reductions.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "qsgd_ops.h"
+
+namespace qsgd {
+namespace ops {
+
+using bf16 = __bf16;
+using f16 = _Float16;
+typedef int v4i __attribute__((ext_vector_type(4)));
+
+// Eight consecutive elements as fp32. The copy carries the element's own
+// alignment, for which gfx950 still issues 16-byte loads (global memory is read
+// at any byte address).
+template <class T>
+__device__ __forceinline__ void load8(const T *p, float (&f)[8]) {
+    T v[8];
+    __builtin_memcpy(v, p, sizeof(v));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = (float)v[i];
+}
+
+// The same, of which only `count` elements (below 8, possibly none) exist; the
+// others read as `fill`.
+template <class T>
+__device__ __forceinline__ void load_part(const T *p, int count, float fill, float (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = i < count ? (float)p[i] : fill;
+}
+
+template <class T>
+__device__ __forceinline__ void load_upto8(const T *p, int64_t left, float fill, float (&f)[8]) {
+    if (left >= 8) load8(p, f);
+    else load_part(p, (int)left, fill, f);
+}
+
+template <class T>
+__device__ __forceinline__ void store8(T *p, const float (&f)[8]) {
+    T v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = (T)f[i];
+    __builtin_memcpy(p, v, sizeof(v));
+}
+
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+#pragma unroll
+    for (int o = 32; o; o >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, o));
+    return v;
+}
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+    for (int o = 32; o; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
+    return v;
+}
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+    for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
+    return v;
+}
+
+// A launch of `blocks` workgroups as a grid of two dimensions (one dimension of a
+// grid holds fewer than 2^32 threads), and the workgroup's number in it, which
+// may be past the last one.
+inline dim3 grid_of(uint64_t blocks) {
+    const uint64_t x = blocks < (1u << 20) ? blocks : (1u << 20);
+    return dim3((uint32_t)x, (uint32_t)((blocks + x - 1) / x));
+}
+__device__ __forceinline__ uint64_t block_index() { return (uint64_t)blockIdx.y * gridDim.x + blockIdx.x; }
+
+inline bool is_float(qsgd_dtype t) { return t == QSGD_F32 || t == QSGD_F16 || t == QSGD_BF16; }
+inline uint64_t bytes_of(qsgd_dtype t) { return t == QSGD_F32 || t == QSGD_I32 ? 4 : t == QSGD_I64 ? 8 : 2; }
+inline bool aligned_to(const void *p, uint64_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+inline uint64_t round_up(uint64_t v, uint64_t to) { return (v + to - 1) / to * to; }
+inline uint64_t div_up(uint64_t v, uint64_t by) { return (v + by - 1) / by; }
+inline qsgd_status launched() { return hipGetLastError() == hipSuccess ? QSGD_OK : QSGD_ERR_LAUNCH; }
+
+constexpr uint64_t kMaxDim = (1ull << 31) - 1;
+
+// Calls f with a value of the element type.
+template <class F>
+qsgd_status with_type(qsgd_dtype t, F f) {
+    switch (t) {
+        case QSGD_F32: return f(float{});
+        case QSGD_F16: return f(f16{});
+        case QSGD_BF16: return f(bf16{});
+        default: return QSGD_ERR_INVALID_ARG;
+    }
+}
+
+}  // namespace ops
+}  // namespace qsgd

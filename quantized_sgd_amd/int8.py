@@ -1,0 +1,160 @@
+"""The 8-bit linear layer: quantizer, product, layer and gradient.
+
+Levels are those of the compressor's max-norm scale with s = 127 and one bucket
+per row (or column), rounded to the nearest; include/qsgd_ops.h has the
+formulas. The weight gradient comes out in fp32, as `encode` takes it.
+"""
+from __future__ import annotations
+
+import ctypes
+import functools
+
+import torch
+
+from ._ops import DTYPE, FLOATS, check, function, matrix, on, raw_stream, same_device, scratch, u64, vector, vp
+
+__all__ = ["int8_quantize", "int8_matmul", "int8_linear", "int8_linear_backward"]
+
+_int = ctypes.c_int
+_I8 = (torch.int8,)
+
+
+@functools.lru_cache(maxsize=1024)
+def _quantize_t_bytes(rows, cols):
+    return function("qsgd_int8_quantize_transposed_workspace", u64, u64, u64)(rows, cols)
+
+
+@functools.lru_cache(maxsize=1024)
+def _matmul_bytes(a_off, lda, b_off, ldb, m, n, k):
+    return function("qsgd_int8_matmul_workspace", u64, vp, u64, vp, u64, u64, u64, u64)(
+        16 + a_off, lda, 16 + b_off, ldb, m, n, k)
+
+
+@functools.lru_cache(maxsize=1024)
+def _linear_bytes(w_off, ldw, m, n, k, keep):
+    return function("qsgd_int8_linear_workspace", u64, vp, u64, u64, u64, u64, _int)(16 + w_off, ldw, m, n, k, keep)
+
+
+@functools.lru_cache(maxsize=1024)
+def _backward_bytes(m, n, k):
+    return function("qsgd_int8_linear_backward_workspace", u64, u64, u64, u64)(m, n, k)
+
+
+def int8_quantize(x: torch.Tensor, fold=None, transpose: bool = False, out=None, scale=None, stream=None):
+    """Levels and scales of x [R, C] (fp32, fp16 or bf16; any row stride): of each
+    row, as (int8 [R, C], fp32 [R]), or with `transpose` of each column, the
+    levels transposed, as (int8 [C, R], fp32 [C]). `fold` (fp32) multiplies x along
+    the reduced axis first: [C], with `transpose` [R]."""
+    ldx = matrix(x, "x", FLOATS)
+    rows, cols = x.shape
+    dev = x.device
+    n, length = (cols, rows) if transpose else (rows, cols)
+    f = vector(fold, "fold", length, dev)
+    with on(dev, stream):
+        if out is None:
+            out = torch.empty(n, length, dtype=torch.int8, device=dev)
+        if scale is None:
+            scale = torch.empty(n, dtype=torch.float32, device=dev)
+        ldl = matrix(out, "out", _I8, n, length)
+        same_device(dev, out=out)
+        s = vector(scale, "scale", n, dev)
+        if transpose:
+            ws = scratch(_quantize_t_bytes(rows, cols), dev)
+            check(function("qsgd_int8_quantize_transposed", _int, vp, _int, u64, u64, u64, vp, vp, u64, vp, vp, vp)(
+                x.data_ptr(), DTYPE[x.dtype], rows, cols, ldx, f, out.data_ptr(), max(ldl, length), s,
+                None if ws is None else ws.data_ptr(), raw_stream(dev)), "qsgd_int8_quantize_transposed")
+        else:
+            check(function("qsgd_int8_quantize", _int, vp, _int, u64, u64, u64, vp, vp, u64, vp, vp)(
+                x.data_ptr(), DTYPE[x.dtype], rows, cols, ldx, f, out.data_ptr(), ldl, s, raw_stream(dev)),
+                "qsgd_int8_quantize")
+    return out, scale
+
+
+def int8_matmul(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb=None, bias=None, dtype=torch.bfloat16, out=None,
+                stream=None):
+    """y [M, N] = (a b^T) with a scale for each row of a [M, K] (sa) and of b [N, K]
+    (sb, or None for 1), plus bias [N] if given, in `dtype` (or out's). a and b are
+    int8 with any row stride; the sum over K is exact."""
+    lda = matrix(a, "a", _I8)
+    m, k = a.shape
+    ldb = matrix(b, "b", _I8, None, k)
+    n = b.shape[0]
+    dev = a.device
+    same_device(dev, b=b)
+    if sa is None:
+        raise ValueError("sa must be a tensor")
+    pa, pb, pbias = vector(sa, "sa", m, dev), vector(sb, "sb", n, dev), vector(bias, "bias", n, dev)
+    with on(dev, stream):
+        if out is None:
+            out = torch.empty(m, n, dtype=dtype, device=dev)
+        ldy = matrix(out, "out", FLOATS, m, n)
+        same_device(dev, out=out)
+        ap, bp = a.data_ptr(), b.data_ptr()
+        ws = scratch(_matmul_bytes(ap & 15, lda, bp & 15, ldb, m, n, k), dev)
+        check(function("qsgd_int8_matmul", _int, vp, u64, vp, vp, u64, vp, vp, vp, _int, u64, u64, u64, u64, vp, vp)(
+            ap, lda, pa, bp, ldb, pb, pbias, out.data_ptr(), DTYPE[out.dtype], ldy, m, n, k,
+            None if ws is None else ws.data_ptr(), raw_stream(dev)), "qsgd_int8_matmul")
+    return out
+
+
+def int8_linear(x: torch.Tensor, w: torch.Tensor, sw: torch.Tensor, bias=None, keep: bool = False, out=None, stream=None):
+    """The layer y [M, N] = x w^T with x [M, K] (fp32, fp16 or bf16) quantized per
+    row on the way, w [N, K] the weight's levels, sw [N] their scales, in x's type.
+    With `keep`, returns (y, xq, sx): xq the levels of x (a view with rows padded to
+    16) and sx their scales, which int8_linear_backward takes."""
+    ldx = matrix(x, "x", FLOATS)
+    m, k = x.shape
+    ldw = matrix(w, "w", _I8, None, k)
+    n = w.shape[0]
+    dev = x.device
+    same_device(dev, w=w)
+    if sw is None:
+        raise ValueError("sw must be a tensor")
+    psw, pbias = vector(sw, "sw", n, dev), vector(bias, "bias", n, dev)
+    with on(dev, stream):
+        if out is None:
+            out = torch.empty(m, n, dtype=x.dtype, device=dev)
+        ldy = matrix(out, "out", (x.dtype,), m, n)
+        same_device(dev, out=out)
+        wp = w.data_ptr()
+        xq = sx = None
+        ldq = 0
+        if keep:
+            ldq = max(16, (k + 15) // 16 * 16)
+            xq = torch.empty(m, ldq, dtype=torch.int8, device=dev)
+            sx = torch.empty(m, dtype=torch.float32, device=dev)
+        ws = scratch(_linear_bytes(wp & 15, ldw, m, n, k, int(keep)), dev)
+        check(function("qsgd_int8_linear", _int, vp, _int, u64, vp, u64, vp, vp, vp, u64, vp, u64, vp, u64, u64, u64, vp,
+                       vp)(
+            x.data_ptr(), DTYPE[x.dtype], ldx, wp, ldw, psw, pbias, out.data_ptr(), ldy,
+            xq.data_ptr() if keep else None, ldq, sx.data_ptr() if keep else None, m, n, k,
+            None if ws is None else ws.data_ptr(), raw_stream(dev)), "qsgd_int8_linear")
+    return (out, xq[:, :k], sx) if keep else out
+
+
+def int8_linear_backward(gy: torch.Tensor, xq: torch.Tensor, sx: torch.Tensor, w: torch.Tensor, sw: torch.Tensor,
+                         need_gx: bool = True, need_gw: bool = True, stream=None):
+    """The gradient of int8_linear for gy [M, N]: gx [M, K] in gy's type, with
+    respect to x (straight through its rounding), and gw [N, K] in fp32, with
+    respect to the real weight sw w. gy is held in 8 bits for both (per row for
+    gx, per column for gw). Returns (gx, gw), None for one not needed."""
+    ldg = matrix(gy, "gy", FLOATS)
+    m, n = gy.shape
+    ldq = matrix(xq, "xq", _I8, m, None)
+    k = xq.shape[1]
+    ldw = matrix(w, "w", _I8, n, k)
+    dev = gy.device
+    same_device(dev, xq=xq, w=w)
+    if sx is None or sw is None:
+        raise ValueError("sx and sw must be tensors")
+    psx, psw = vector(sx, "sx", m, dev), vector(sw, "sw", n, dev)
+    with on(dev, stream):
+        gx = torch.empty(m, k, dtype=gy.dtype, device=dev) if need_gx else None
+        gw = torch.empty(n, k, dtype=torch.float32, device=dev) if need_gw else None
+        ws = scratch(_backward_bytes(m, n, k), dev)
+        check(function("qsgd_int8_linear_backward", _int, vp, _int, u64, vp, u64, vp, vp, u64, vp, vp, u64, vp, u64, u64,
+                       u64, u64, vp, vp)(
+            gy.data_ptr(), DTYPE[gy.dtype], ldg, xq.data_ptr(), ldq, psx, w.data_ptr(), ldw, psw,
+            gx.data_ptr() if need_gx else None, max(k, 1), gw.data_ptr() if need_gw else None, max(k, 1), m, n, k,
+            None if ws is None else ws.data_ptr(), raw_stream(dev)), "qsgd_int8_linear_backward")
+    return gx, gw

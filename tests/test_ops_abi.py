@@ -1,0 +1,75 @@
+"""The operators' C ABI on the CPU: exports, workspace sizes and the refusals that
+come before anything touches a device."""
+import os
+import re
+
+import pytest
+import torch
+
+import quantized_sgd_amd as q
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+INVALID, UNSUPPORTED = q.QSGD_ERR_INVALID_ARG, q.QSGD_ERR_UNSUPPORTED
+
+
+def test_every_declared_function_is_exported():
+    text = open(os.path.join(ROOT, "include", "qsgd_ops.h")).read()
+    text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
+    names = sorted(set(re.findall(r"\b(qsgd_(?:int8|distill)[a-z0-9_]*)\s*\(", text)))
+    assert len(names) >= 8
+    for name in names:
+        assert hasattr(q.lib(), name), name
+
+
+def test_int8_argument_checks():
+    from quantized_sgd_amd import int8  # noqa: F401 (its C types are set on use)
+    from quantized_sgd_amd._ops import function, u64, vp
+    import ctypes
+    i = ctypes.c_int
+    quant = function("qsgd_int8_quantize", i, vp, i, u64, u64, u64, vp, vp, u64, vp, vp)
+    assert quant(16, 0, 0, 8, 8, None, 16, 8, 16, None) == 0             # no rows
+    assert quant(16, 3, 4, 8, 8, None, 16, 8, 16, None) == INVALID       # an integer type
+    assert quant(16, 0, 4, 8, 7, None, 16, 8, 16, None) == INVALID       # overlapping rows of x
+    assert quant(16, 0, 4, 8, 8, None, 16, 7, 16, None) == INVALID       # overlapping rows of levels
+    assert quant(None, 0, 4, 8, 8, None, 16, 8, 16, None) == INVALID
+    assert quant(16, 0, 4, 8, 8, None, 16, 8, None, None) == INVALID
+    assert quant(16, 0, 1 << 31, 8, 8, None, 16, 8, 16, None) == INVALID
+    size_t = function("qsgd_int8_quantize_transposed_workspace", u64, u64, u64)
+    assert size_t(100, 0) == 0 and size_t(0, 100) >= 400 and size_t(4096, 4096) >= 4 * 4096
+    quant_t = function("qsgd_int8_quantize_transposed", i, vp, i, u64, u64, u64, vp, vp, u64, vp, vp, vp)
+    assert quant_t(16, 0, 8, 0, 8, None, 16, 8, 16, None, None) == 0     # no columns
+    assert quant_t(16, 0, 8, 4, 4, None, 16, 8, 16, None, None) == INVALID   # no workspace
+    assert quant_t(16, 0, 8, 4, 4, None, 16, 8, 16, 8, None) == INVALID      # misaligned workspace
+    assert quant_t(16, 0, 8, 4, 4, None, 16, 7, 16, 16, None) == INVALID
+    mm = function("qsgd_int8_matmul", i, vp, u64, vp, vp, u64, vp, vp, vp, i, u64, u64, u64, u64, vp, vp)
+    assert mm(16, 8, 16, 16, 8, None, None, 16, 0, 5, 0, 5, 8, None, None) == 0
+    assert mm(16, 8, 16, 16, 8, None, None, 16, 0, 5, 4, 5, 9, None, None) == INVALID   # rows shorter than k
+    assert mm(16, 8, 16, 16, 8, None, None, 16, 0, 4, 4, 5, 8, None, None) == INVALID   # rows of y shorter than n
+    assert mm(16, 8, None, 16, 8, None, None, 16, 0, 5, 4, 5, 8, None, None) == INVALID
+    assert mm(16, 8, 16, 16, 8, None, None, 16, 4, 5, 4, 5, 8, None, None) == INVALID   # y of integers
+    big = (1 << 23) + 16
+    assert mm(16, big, 16, 16, big, None, None, 16, 0, 5, 4, 5, big, None, None) == UNSUPPORTED
+    assert mm(16, 33, 16, 16, 33, None, None, 16, 0, 500, 400, 500, 33, None, None) == INVALID  # odd rows, no workspace
+    size = function("qsgd_int8_matmul_workspace", u64, vp, u64, vp, u64, u64, u64, u64)
+    assert size(16, 4096, 16, 4096, 8192, 8192, 4096) == 0
+    assert size(16, 4096, 17, 4096, 8192, 8192, 4096) >= 8192 * 4096       # b is copied to aligned rows
+    assert size(16, 65536, 16, 65536, 64, 64, 65536) >= 2 * 64 * 64 * 4    # the sum is split
+    lin = function("qsgd_int8_linear", i, vp, i, u64, vp, u64, vp, vp, vp, u64, vp, u64, vp, u64, u64, u64, vp, vp)
+    assert lin(16, 0, 8, 16, 8, 16, None, 16, 5, None, 0, None, 0, 5, 8, None, None) == 0
+    assert lin(16, 0, 8, 16, 8, 16, None, 16, 5, None, 0, None, 4, 5, 8, None, None) == INVALID  # no workspace
+    assert lin(16, 0, 8, 16, 8, 16, None, 16, 5, 16, 16, None, 4, 5, 8, None, None) == INVALID   # xq without sx
+    assert lin(16, 0, 8, 16, 8, 16, None, 16, 5, 16, 8, 16, 4, 5, 8, None, None) == INVALID      # rows of xq not padded
+    assert lin(16, 0, 8, 16, 8, 16, None, 16, 5, 24, 16, 16, 4, 5, 8, None, None) == INVALID     # xq not aligned
+    back = function("qsgd_int8_linear_backward", i, vp, i, u64, vp, u64, vp, vp, u64, vp, vp, u64, vp, u64, u64, u64, u64,
+                    vp, vp)
+    assert back(16, 0, 5, 16, 8, 16, 16, 8, 16, None, 8, None, 8, 4, 5, 8, 16, None) == 0        # neither is wanted
+    assert back(16, 0, 5, 16, 8, 16, 16, 8, 16, 16, 8, 16, 8, 4, 5, 8, None, None) == INVALID    # no workspace
+    assert back(16, 0, 4, 16, 8, 16, 16, 8, 16, 16, 8, 16, 8, 4, 5, 8, 16, None) == INVALID
+    assert back(16, 0, 5, 16, 8, 16, 16, 8, 16, 16, 7, 16, 8, 4, 5, 8, 16, None) == INVALID
+
+
+def test_bindings_refuse_host_tensors():
+    with pytest.raises(ValueError):
+        q.int8_quantize(torch.zeros(2, 3))
+    with pytest.raises(ValueError):
+        q.int8_matmul(torch.zeros(2, 3, dtype=torch.int8), torch.ones(2), torch.zeros(4, 3, dtype=torch.int8))
