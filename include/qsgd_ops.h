@@ -116,6 +116,66 @@ qsgd_status qsgd_int8_linear_backward(const void *gy, qsgd_dtype dtype, uint64_t
                                       const float *sw, void *gx, uint64_t ldgx, float *gw, uint64_t ldgw,
                                       uint64_t m, uint64_t n, uint64_t k, void *workspace, hipStream_t stream);
 
+/* ---- distillation from a teacher's top logits ------------------------------
+ * A row is a position with student logits z[0..vocab) and k entries (index, teacher
+ * logit t). An index below 0, or at or past the vocabulary, is no entry; the others
+ * of a row must differ from each other. With q = softmax(z / tau) over the whole
+ * vocabulary:
+ *   without teacher_lse: p = softmax(t / tau) over the row's entries,
+ *     loss = sum p (log p - log q),   dz_j = g / tau (q_j - p_j);
+ *   with teacher_lse (the logsumexp of the teacher's whole row of logits / tau):
+ *     p = exp(t / tau - teacher_lse), and what is left of the teacher's mass, p_r =
+ *     max(0, 1 - sum p), is held against the student's mass outside the entries,
+ *     q_r: loss = sum p (log p - log q) + p_r (log p_r - log q_r),
+ *     dz_j = g / tau (q_j - p_j) at the entries, g / tau (q_j - p_r q_j / q_r) elsewhere.
+ *     The term of p_r is left out where q_r is 0 (no logit above minus infinity
+ *     outside the entries).
+ * Terms with p = 0 are 0. A row without entries has loss 0 and gradient 0, whatever
+ * its logits; a row with g = 0 has gradient 0. Logits of minus infinity are
+ * vocabulary that the student does not have (an entry there with p > 0 gives an
+ * infinite loss); a row of nothing else has q = 0 and an infinite loss. NaN and plus
+ * infinity give NaN in that row. Statistics and sums are kept in fp32 or wider; the
+ * loss is fp32 and the gradient is rounded once to the type of z.
+ *   z      [rows, vocab] of `dtype` (QSGD_F32, QSGD_F16 or QSGD_BF16), row stride ldz.
+ *   idx    [rows, k] of `itype` (QSGD_I32 or QSGD_I64), row stride ldi.
+ *   t      [rows, k] of `ttype` (a type of z's list), row stride ldt.
+ *   k      at most qsgd_distill_max_entries(); 0 makes every row one without entries.
+ *   tau    1e-30 to 1e30.
+ *   teacher_lse  [rows] fp32 or NULL.
+ *   grad   [rows] fp32 (g, the gradient with respect to each row's loss) or NULL (1).
+ *   loss   [rows] fp32 output.
+ *   stats  [rows, 4] fp32, 16-byte aligned: an output of the forward call that the
+ *          backward call takes, with the same z, idx, t, tau and teacher_lse.
+ *   dz     [rows, vocab] output of z's type, row stride lddz; may be z itself
+ *          (same pointer and stride), not otherwise overlap it.
+ *   workspace  qsgd_distill_workspace(rows, vocab) bytes.
+ */
+uint32_t qsgd_distill_max_entries(void);
+uint64_t qsgd_distill_workspace(uint64_t rows, uint64_t vocab);
+
+/* The entries of a call and how they are read. */
+typedef struct {
+    const void *idx, *t;
+    qsgd_dtype itype, ttype;
+    uint64_t ldi, ldt;
+    uint32_t k;
+    float tau;
+    const float *teacher_lse;
+} qsgd_teacher;
+
+/* Loss of each row. */
+qsgd_status qsgd_distill_forward(const void *z, qsgd_dtype dtype, uint64_t rows, uint64_t vocab, uint64_t ldz,
+                                 const qsgd_teacher *teacher, float *loss, float *stats, void *workspace,
+                                 hipStream_t stream);
+/* Gradient with respect to z, from the forward call's stats. */
+qsgd_status qsgd_distill_backward(const void *z, qsgd_dtype dtype, uint64_t rows, uint64_t vocab, uint64_t ldz,
+                                  const qsgd_teacher *teacher, const float *stats, const float *grad, void *dz,
+                                  uint64_t lddz, hipStream_t stream);
+/* Both at once, for gradients that do not depend on the losses. */
+qsgd_status qsgd_distill_step(const void *z, qsgd_dtype dtype, uint64_t rows, uint64_t vocab, uint64_t ldz,
+                              const qsgd_teacher *teacher, const float *grad, float *loss, void *dz, uint64_t lddz,
+                              void *workspace, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -21,6 +21,7 @@ __all__ = [
     "max_bucket", "max_streams", "decode_accumulate", "decode_accumulate_ragged", "OMEGA", "GAMMA",
     "L2", "MAXNORM", "encode_noalloc", "encode_noalloc_capacity_words", "quantize_seglen", "encode_seglen",
     "decode_seglen", "int8_quantize", "int8_matmul", "int8_linear", "int8_linear_backward",
+    "distill_topk", "distill_topk_backward", "distill_topk_step",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -440,4 +441,5 @@ def decode_seglen(words: torch.Tensor, offsets: torch.Tensor, seg_len, s: int, d
     return v_hat[:n]
 
 
+from .distill import distill_topk, distill_topk_backward, distill_topk_step  # noqa: E402
 from .int8 import int8_linear, int8_linear_backward, int8_matmul, int8_quantize  # noqa: E402

@@ -13,7 +13,7 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libqsgd.so")
-SOURCES = [os.path.join(HERE, "csrc", f) for f in ("qsgd_api.hip", "int8_api.hip")]
+SOURCES = [os.path.join(HERE, "csrc", f) for f in ("qsgd_api.hip", "int8_api.hip", "distill_api.hip")]
 ARCH = os.environ.get("QSGD_OFFLOAD_ARCH", "gfx950")
 
 

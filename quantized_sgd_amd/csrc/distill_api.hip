@@ -1,0 +1,139 @@
+// Host side of the distillation loss (include/qsgd_ops.h): argument checks, the
+// split of rows into segments, launches.
+#include "qsgd_ops.h"
+
+#include <algorithm>
+
+#include "distill.h"
+
+using namespace qsgd::ops;
+
+namespace {
+
+struct Split {
+    uint32_t segments, segment;
+};
+
+// One workgroup a row where there are rows enough for the chip; else segments of
+// at least 8192 logits. The gradient's segments may differ from the loss's.
+Split split_rows(uint64_t rows, uint64_t vocab) {
+    uint64_t segments = std::max<uint64_t>(1, div_up(vocab, kMaxSegment));
+    if (rows < 256) segments = std::max(segments, std::min(div_up(512, std::max<uint64_t>(rows, 1)), vocab / 8192));
+    const uint64_t segment = round_up(std::max<uint64_t>(1, div_up(vocab, segments)), 8);
+    return {(uint32_t)std::max<uint64_t>(1, div_up(vocab, segment)), (uint32_t)segment};
+}
+
+bool args_ok(const void *z, qsgd_dtype dtype, uint64_t rows, uint64_t vocab, uint64_t ldz, const qsgd_teacher *te) {
+    if (!is_float(dtype) || rows > kMaxDim || vocab > kMaxDim || ldz < vocab || !te) return false;
+    if (!(te->tau >= 1e-30f && te->tau <= 1e30f) || te->k > (uint32_t)kMaxEntries) return false;
+    if (te->k && ((te->itype != QSGD_I32 && te->itype != QSGD_I64) || !is_float(te->ttype) || te->ldi < te->k || te->ldt < te->k))
+        return false;
+    if (rows == 0) return true;
+    return (!vocab || z) && (!te->k || (te->idx && te->t));
+}
+
+DistillParams params_of(const void *z, uint64_t rows, uint64_t vocab, uint64_t ldz, const qsgd_teacher *te) {
+    DistillParams p{};
+    p.z = z;
+    p.idx = te->idx;
+    p.t = te->t;
+    p.teacher_lse = te->teacher_lse;
+    p.ldz = ldz;
+    p.ldi = te->ldi;
+    p.ldt = te->ldt;
+    p.rows = (uint32_t)rows;
+    p.vocab = (uint32_t)vocab;
+    p.k = te->k;
+    p.itype = te->itype;
+    p.ttype = te->ttype;
+    p.inv_tau = 1.0f / te->tau;
+    const Split s = split_rows(rows, vocab);
+    p.segments = s.segments;
+    p.segment = s.segment;
+    return p;
+}
+
+// Workspace of a split: the segments' pairs, then a row's statistics.
+uint64_t pair_bytes(const DistillParams &p) { return round_up((uint64_t)p.rows * p.segments * 8, 256); }
+
+template <class T>
+void launch_stats(DistillParams p, void *workspace, hipStream_t stream) {
+    p.part = (float2 *)workspace;
+    distill_part_kernel<T><<<grid_of((uint64_t)p.rows * p.segments), kDT, 0, stream>>>(p);
+    distill_join_kernel<T><<<grid_of(p.rows), 256, 0, stream>>>(p);
+}
+
+}  // namespace
+
+extern "C" {
+
+uint32_t qsgd_distill_max_entries(void) { return kMaxEntries; }
+
+uint64_t qsgd_distill_workspace(uint64_t rows, uint64_t vocab) {
+    if (rows > kMaxDim || vocab > kMaxDim || rows == 0) return 0;
+    const Split s = split_rows(rows, vocab);
+    return s.segments == 1 ? 0 : round_up(rows * s.segments * 8, 256) + rows * 16;
+}
+
+qsgd_status qsgd_distill_forward(const void *z, qsgd_dtype dtype, uint64_t rows, uint64_t vocab, uint64_t ldz,
+                                 const qsgd_teacher *teacher, float *loss, float *stats, void *workspace,
+                                 hipStream_t stream) {
+    if (!args_ok(z, dtype, rows, vocab, ldz, teacher)) return QSGD_ERR_INVALID_ARG;
+    if (rows == 0) return QSGD_OK;
+    if (!loss || !stats || !aligned_to(stats, 16)) return QSGD_ERR_INVALID_ARG;
+    DistillParams p = params_of(z, rows, vocab, ldz, teacher);
+    if (p.segments > 1 && (!workspace || !aligned_to(workspace, 16))) return QSGD_ERR_INVALID_ARG;
+    p.loss = loss;
+    p.stats = stats;
+    return with_type(dtype, [&](auto t) {
+        using T = decltype(t);
+        if (p.segments == 1) distill_row_kernel<T, false><<<grid_of(rows), kDT, 0, stream>>>(p);
+        else launch_stats<T>(p, workspace, stream);
+        return launched();
+    });
+}
+
+qsgd_status qsgd_distill_backward(const void *z, qsgd_dtype dtype, uint64_t rows, uint64_t vocab, uint64_t ldz,
+                                  const qsgd_teacher *teacher, const float *stats, const float *grad, void *dz,
+                                  uint64_t lddz, hipStream_t stream) {
+    if (!args_ok(z, dtype, rows, vocab, ldz, teacher) || lddz < vocab) return QSGD_ERR_INVALID_ARG;
+    if (rows == 0 || vocab == 0) return QSGD_OK;
+    if (!dz || !stats || !aligned_to(stats, 16)) return QSGD_ERR_INVALID_ARG;
+    DistillParams p = params_of(z, rows, vocab, ldz, teacher);
+    p.stats_in = stats;
+    p.grad = grad;
+    p.dz = dz;
+    p.lddz = lddz;
+    return with_type(dtype, [&](auto t) {
+        distill_gradient_kernel<decltype(t)><<<grid_of(rows * p.segments), kDT, 0, stream>>>(p);
+        return launched();
+    });
+}
+
+qsgd_status qsgd_distill_step(const void *z, qsgd_dtype dtype, uint64_t rows, uint64_t vocab, uint64_t ldz,
+                              const qsgd_teacher *teacher, const float *grad, float *loss, void *dz, uint64_t lddz,
+                              void *workspace, hipStream_t stream) {
+    if (!args_ok(z, dtype, rows, vocab, ldz, teacher) || lddz < vocab) return QSGD_ERR_INVALID_ARG;
+    if (rows == 0) return QSGD_OK;
+    if (!loss || (vocab && !dz)) return QSGD_ERR_INVALID_ARG;
+    DistillParams p = params_of(z, rows, vocab, ldz, teacher);
+    if (p.segments > 1 && (!workspace || !aligned_to(workspace, 16))) return QSGD_ERR_INVALID_ARG;
+    p.loss = loss;
+    p.grad = grad;
+    p.dz = dz;
+    p.lddz = lddz;
+    return with_type(dtype, [&](auto t) {
+        using T = decltype(t);
+        if (p.segments == 1) {
+            distill_row_kernel<T, true><<<grid_of(rows), kDT, 0, stream>>>(p);
+        } else {
+            p.stats = (float *)((char *)workspace + pair_bytes(p));
+            p.stats_in = p.stats;
+            launch_stats<T>(p, workspace, stream);
+            distill_gradient_kernel<T><<<grid_of((uint64_t)p.rows * p.segments), kDT, 0, stream>>>(p);
+        }
+        return launched();
+    });
+}
+
+}  // extern "C"

@@ -1,0 +1,119 @@
+"""Distillation from a teacher's top logits: the loss of each position and its
+gradient with respect to the student's logits. include/qsgd_ops.h has the
+formulas and what is done with masked vocabulary, rows without entries, infinities
+and NaN.
+"""
+from __future__ import annotations
+
+import ctypes
+import functools
+
+import torch
+
+from ._ops import DTYPE, FLOATS, check, function, matrix, on, raw_stream, same_device, scratch, u64, vector, vp
+
+__all__ = ["distill_topk", "distill_topk_backward", "distill_topk_step"]
+
+_int = ctypes.c_int
+_INDEX = (torch.int32, torch.int64)
+
+
+class _Teacher(ctypes.Structure):
+    _fields_ = [("idx", vp), ("t", vp), ("itype", _int), ("ttype", _int), ("ldi", u64), ("ldt", u64),
+                ("k", ctypes.c_uint32), ("tau", ctypes.c_float), ("teacher_lse", vp)]
+
+
+_teacher_p = ctypes.POINTER(_Teacher)
+
+
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes(rows, vocab):
+    return function("qsgd_distill_workspace", u64, u64, u64)(rows, vocab)
+
+
+def _teacher(z, idx, t, tau, teacher_lse):
+    """Checks the inputs that all calls share; returns z's row stride and the
+    entries' description."""
+    ldz = matrix(z, "z", FLOATS)
+    rows, dev = z.shape[0], z.device
+    ldi = matrix(idx, "idx", _INDEX, rows, None)
+    k = idx.shape[1]
+    ldt = matrix(t, "t", FLOATS, rows, k)
+    same_device(dev, idx=idx, t=t)
+    lse = vector(teacher_lse, "teacher_lse", rows, dev)
+    most = function("qsgd_distill_max_entries", ctypes.c_uint32)()
+    if k > most:
+        raise ValueError(f"at most {most} entries a row, got {k}")
+    if not 1e-30 <= tau <= 1e30:
+        raise ValueError(f"tau must be between 1e-30 and 1e30, got {tau}")
+    return ldz, _Teacher(idx.data_ptr(), t.data_ptr(), DTYPE[idx.dtype], DTYPE[t.dtype], ldi, ldt, k, tau, lse)
+
+
+def _gradient_out(z, ldz, out):
+    if out is None:
+        out = torch.empty(z.shape, dtype=z.dtype, device=z.device)
+    ld = matrix(out, "out", (z.dtype,), *z.shape)
+    same_device(z.device, out=out)
+    if out.data_ptr() == z.data_ptr() and ld != ldz:
+        raise ValueError("out in z's place must have z's row stride")
+    return out, ld
+
+
+def distill_topk(z: torch.Tensor, idx: torch.Tensor, t: torch.Tensor, tau: float = 1.0, teacher_lse=None, stream=None):
+    """The loss of each row (fp32 [T]) of student logits z [T, V] against the
+    teacher's logits t [T, k] at idx [T, k] (int32 or int64; an index outside the
+    vocabulary is no entry; a row's indices differ). Without teacher_lse the
+    teacher's distribution is the softmax over the entries; with it (fp32 [T], the
+    logsumexp of the teacher's whole row of logits / tau) the mass that the entries
+    leave is held against the student's mass outside them. Returns (loss, stats);
+    distill_topk_backward takes the stats."""
+    ldz, te = _teacher(z, idx, t, tau, teacher_lse)
+    rows, vocab = z.shape
+    dev = z.device
+    with on(dev, stream):
+        loss = torch.empty(rows, dtype=torch.float32, device=dev)
+        stats = torch.empty(rows, 4, dtype=torch.float32, device=dev)
+        ws = scratch(_workspace_bytes(rows, vocab), dev)
+        check(function("qsgd_distill_forward", _int, vp, _int, u64, u64, u64, _teacher_p, vp, vp, vp, vp)(
+            z.data_ptr(), DTYPE[z.dtype], rows, vocab, ldz, te, loss.data_ptr(), stats.data_ptr(),
+            None if ws is None else ws.data_ptr(), raw_stream(dev)), "qsgd_distill_forward")
+    return loss, stats
+
+
+def distill_topk_backward(z: torch.Tensor, idx: torch.Tensor, t: torch.Tensor, stats: torch.Tensor, grad_loss=None,
+                          tau: float = 1.0, teacher_lse=None, out=None, stream=None):
+    """The gradient with respect to z, in its type: grad_loss [T] (fp32; None for 1)
+    is that with respect to the losses, stats is the forward call's, the other
+    arguments are the same. `out` may be z."""
+    ldz, te = _teacher(z, idx, t, tau, teacher_lse)
+    rows, vocab = z.shape
+    dev = z.device
+    matrix(stats, "stats", (torch.float32,), rows, 4)
+    same_device(dev, stats=stats)
+    if not stats.is_contiguous():
+        raise ValueError("stats must be contiguous")
+    g = vector(grad_loss, "grad_loss", rows, dev)
+    with on(dev, stream):
+        out, ld = _gradient_out(z, ldz, out)
+        check(function("qsgd_distill_backward", _int, vp, _int, u64, u64, u64, _teacher_p, vp, vp, vp, u64, vp)(
+            z.data_ptr(), DTYPE[z.dtype], rows, vocab, ldz, te, stats.data_ptr(), g, out.data_ptr(), ld,
+            raw_stream(dev)), "qsgd_distill_backward")
+    return out
+
+
+def distill_topk_step(z: torch.Tensor, idx: torch.Tensor, t: torch.Tensor, grad_loss=None, tau: float = 1.0,
+                      teacher_lse=None, out=None, stream=None):
+    """Loss and gradient in one call, for a grad_loss that does not depend on the
+    losses (row weights). Returns (loss, dz); `out` may be z."""
+    ldz, te = _teacher(z, idx, t, tau, teacher_lse)
+    rows, vocab = z.shape
+    dev = z.device
+    g = vector(grad_loss, "grad_loss", rows, dev)
+    with on(dev, stream):
+        out, ld = _gradient_out(z, ldz, out)
+        loss = torch.empty(rows, dtype=torch.float32, device=dev)
+        ws = scratch(_workspace_bytes(rows, vocab), dev)
+        check(function("qsgd_distill_step", _int, vp, _int, u64, u64, u64, _teacher_p, vp, vp, vp, u64, vp, vp)(
+            z.data_ptr(), DTYPE[z.dtype], rows, vocab, ldz, te, g, loss.data_ptr(), out.data_ptr(), ld,
+            None if ws is None else ws.data_ptr(), raw_stream(dev)), "qsgd_distill_step")
+    return loss, out

@@ -73,3 +73,32 @@ def test_bindings_refuse_host_tensors():
         q.int8_quantize(torch.zeros(2, 3))
     with pytest.raises(ValueError):
         q.int8_matmul(torch.zeros(2, 3, dtype=torch.int8), torch.ones(2), torch.zeros(4, 3, dtype=torch.int8))
+
+
+def test_distill_argument_checks():
+    import ctypes
+
+    from quantized_sgd_amd._ops import function, u64, vp
+    from quantized_sgd_amd.distill import _Teacher, _teacher_p
+    i = ctypes.c_int
+    step = function("qsgd_distill_step", i, vp, i, u64, u64, u64, _teacher_p, vp, vp, vp, u64, vp, vp)
+
+    def call(te, dtype=0, rows=300, ldz=100, z=16, loss=16, dz=16, lddz=100, vocab=100):
+        return step(z, dtype, rows, vocab, ldz, te, None, loss, dz, lddz, None, None)
+
+    def teacher(idx=16, t=16, itype=3, ttype=0, ldi=5, ldt=5, k=5, tau=1.0):
+        return _Teacher(idx, t, itype, ttype, ldi, ldt, k, tau, None)
+
+    assert call(teacher(), rows=0) == 0
+    for te in (None, teacher(itype=0), teacher(ttype=3), teacher(ldi=4), teacher(ldt=4), teacher(k=1025, ldi=1025, ldt=1025),
+               teacher(tau=0.0), teacher(tau=float("nan")), teacher(tau=float("inf")), teacher(idx=None), teacher(t=None)):
+        assert call(te) == INVALID
+    te = teacher()
+    assert call(te, dtype=4) == INVALID and call(te, ldz=99) == INVALID and call(te, lddz=99) == INVALID
+    assert call(te, z=None) == INVALID and call(te, loss=None) == INVALID and call(te, dz=None) == INVALID
+    size = function("qsgd_distill_workspace", u64, u64, u64)
+    assert size(4096, 131072) == 0 and size(0, 131072) == 0
+    assert size(2, 131072) > 0 and size(4096, 300000) > 0          # rows split into segments
+    assert call(te, rows=2, vocab=131072, ldz=131072, lddz=131072) == INVALID  # no workspace
+    back = function("qsgd_distill_backward", i, vp, i, u64, u64, u64, _teacher_p, vp, vp, vp, u64, vp)
+    assert back(16, 0, 3, 100, 100, te, 8, None, 16, 100, None) == INVALID     # misaligned stats
