@@ -74,12 +74,12 @@ qsgd_status transpose_bytes(const int8_t *x, uint64_t rows, uint64_t cols, uint6
 
 // ---- product ----
 
-using Tile256 = Tile<2, 2, 8, 8, 4>;
-using Tile128 = Tile<2, 2, 4, 4, 4>;
-using Tile64 = Tile<2, 2, 2, 2, 4>;
+using Tile256 = Tile<2, 2, 8, 8, 2>;
+using Tile128 = Tile<2, 2, 4, 4, 2>;
+using Tile64 = Tile<2, 2, 2, 2, 3>;
 
 constexpr uint64_t kMaxK = 1u << 23;  // a tile's row offsets are 32-bit
-constexpr uint64_t kSafeSteps = 2047; // 64-byte steps whose sum of products stays below 2^31 (2047 * 64 * 128^2)
+constexpr uint64_t kSafeSteps = 1023; // 128-byte steps whose sum of products stays below 2^31 (1023 * 128 * 128^2)
 constexpr uint64_t kCus = 256;
 
 struct Plan {
@@ -101,12 +101,12 @@ Plan plan_matmul(bool a_aligned, uint64_t lda, bool a_padded, bool b_aligned, ui
     Plan p;
     p.lda = lda;
     p.ldb = ldb;
-    const uint64_t all = std::max<uint64_t>(1, div_up(k, 64));
+    const uint64_t all = std::max<uint64_t>(1, div_up(k, 128));
     if (m <= 32 && n <= (1u << 24) && all <= kSafeSteps) {
         p.skinny = true;
         return p;
     }
-    const uint64_t kp = round_up(std::max<uint64_t>(k, 1), 64);
+    const uint64_t kp = round_up(std::max<uint64_t>(k, 1), 128);
     if (!loads_as_is(a_aligned, lda, k, a_padded)) {
         p.repack_a = true;
         p.lda = kp;
@@ -126,7 +126,7 @@ Plan plan_matmul(bool a_aligned, uint64_t lda, bool a_padded, bool b_aligned, ui
     p.tiles_n = div_up(n, side[p.tile]);
     const uint64_t tiles = p.tiles_m * p.tiles_n;
     uint64_t splits = div_up(all, kSafeSteps);
-    if (tiles < kCus) splits = std::max(splits, std::min({kCus / tiles, all / 8, (uint64_t)16}));
+    if (tiles < kCus) splits = std::max(splits, std::min({kCus / tiles, all / 4, (uint64_t)16}));
     p.steps = div_up(all, splits);
     p.splits = div_up(all, p.steps);
     if (p.splits > 1) {

@@ -21,7 +21,7 @@ struct MatmulParams {
     uint64_t lda, ldb, ldy;
     uint32_t m, n, k;
     uint32_t tiles_m, tiles_n;
-    uint32_t splits, steps_per_split;  // 64-byte steps of k
+    uint32_t splits, steps_per_split;  // 128-byte steps of k
 };
 
 // Sixteen zero bytes that tile loads past the end of k are pointed at.
@@ -49,25 +49,25 @@ __device__ __forceinline__ void load_to_lds(uint32_t lds, const int8_t *from) {
                  :: "s"(lds), "v"(from) : "memory");
 }
 
-// Tiles of BM rows of a and BN rows of b. A step is 64 bytes of k. LDS holds a
-// ring of S steps, each BM + BN rows of 64 bytes, loaded straight from memory S - 1
-// steps ahead. A row's four 16-byte chunks are stored in the order chunk ^ (row /
-// 4 % 4), so that the 16 rows that a fragment read takes at one chunk lie in
-// different banks.
+// Tiles of BM rows of a and BN rows of b. A step is 128 bytes of k: a cache line of
+// each row, so that every request to the L2 is a whole line (steps of 64 bytes made
+// nearly twice the requests and were bound by them). LDS holds a ring of S steps,
+// each BM + BN rows of 128 bytes, loaded straight from memory S - 1 steps ahead. A
+// row's eight 16-byte chunks are stored in the order chunk ^ (row / 2 % 8): the 16
+// lanes that a 16-byte LDS read serves at a time (0-3, 12-15 and 20-27 of a wave's
+// first half, and so on) then lie in different banks.
 //
-// b is the first operand of the matrix instruction (its rows become the
-// accumulator's four consecutive elements) and the rows of b are dealt to LDS so
-// that a lane's TN fragments hold 4 TN consecutive columns of y: the epilogue
-// writes 16 bytes or more a lane.
+// b is the first operand of the matrix instruction, so that its rows become a
+// lane's four consecutive accumulators (columns of y).
 template <int WM_, int WN_, int TM_, int TN_, int S_>
 struct Tile {
     static constexpr int WM = WM_, WN = WN_, TM = TM_, TN = TN_, S = S_;
     static constexpr int BM = WM * TM * 16, BN = WN * TN * 16;
     static constexpr int NW = WM * WN;
-    static constexpr int LA = BM / 16 / NW, LB = BN / 16 / NW;  // loads a wave and step
-    static constexpr int kStage = (BM + BN) * 64;
+    static constexpr int LA = BM / 8 / NW, LB = BN / 8 / NW;  // loads a wave and step
+    static constexpr int kStage = (BM + BN) * 128;
     static constexpr int kLds = S * kStage;
-    static_assert(LA * 16 * NW == BM && LB * 16 * NW == BN && kLds <= 160 * 1024, "");
+    static_assert(LA * 8 * NW == BM && LB * 8 * NW == BN && kLds <= 160 * 1024, "");
 };
 
 template <int N>
@@ -75,6 +75,34 @@ __device__ __forceinline__ void wait_tiles() {
     // all but the N newest loads have landed, and this wave's reads of LDS are done
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" :: "i"(N) : "memory");
 }
+
+// acc += b a^T on the matrix unit, the accumulators held where they are: left to
+// itself the compiler gives the instruction's result registers of their own and
+// moves the 256 accumulators of a large tile about in every step. The compiler
+// does not see the instruction in the assembly, so what reads accumulators after
+// it is kept apart by settle(): a result needs up to 18 wait states before another
+// unit may read it. Two products of one accumulator are TM TN - 1 others apart.
+__device__ __forceinline__ void multiply_add(v4i &acc, const v4i &b, const v4i &a) {
+    asm("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(acc) : "v"(b), "v"(a));
+}
+__device__ __forceinline__ void settle() { asm volatile("s_nop 15\n\ts_nop 7" ::: "memory"); }
+__device__ __forceinline__ void settled(v4i &acc) { asm volatile("" : "+a"(acc)); }
+
+// The column of y, within 32, that row i of b's fragment f (of a pair) belongs to.
+// A lane's accumulators of a pair are rows 4 g to 4 g + 3 of both (g = lane / 16), and
+// the four lanes of a row of y should write 64 bytes in a row, 16 each: for y in 32
+// bits those are the rows of one fragment as they come, for 16 bits the pair's eight.
+template <class OUT>
+__device__ __forceinline__ uint32_t column_of(uint32_t f, uint32_t i) {
+    return sizeof(OUT) == 4 ? f * 16 + i : i / 4 * 8 + f * 4 + i % 4;
+}
+
+struct yes {
+    static constexpr bool value = true;
+};
+struct no {
+    static constexpr bool value = false;
+};
 
 template <class C, class OUT>
 __global__ __launch_bounds__(C::NW * 64, 1) void matmul_kernel(MatmulParams p) {
@@ -94,47 +122,49 @@ __global__ __launch_bounds__(C::NW * 64, 1) void matmul_kernel(MatmulParams p) {
     const uint32_t bm = (band * 8 + in_band % band_rows) * C::BM, bn = in_band / band_rows * C::BN;
 
     const uint32_t k0 = blockIdx.y * p.steps_per_split;  // first step
-    const uint32_t all = (p.k + 63) / 64;
+    const uint32_t all = (p.k + 127) / 128;
     const uint32_t steps = min(p.steps_per_split, all - k0);
-    const uint32_t full = min(steps, p.k / 64 - min(p.k / 64, k0));  // steps wholly inside k
+    const uint32_t full = min(steps, p.k / 128 - min(p.k / 128, k0));  // steps wholly inside k
 
-    // This lane's part of the wave's loads. Rows past the end repeat the last one.
-    const int8_t *a = p.a + (uint64_t)bm * p.lda + (uint64_t)k0 * 64;
-    const int8_t *b = p.b + (uint64_t)bn * p.ldb + (uint64_t)k0 * 64;
+    // This lane's part of the wave's loads: eight lanes a row. Rows past the end
+    // repeat the last one.
+    const int8_t *a = p.a + (uint64_t)bm * p.lda + (uint64_t)k0 * 128;
+    const int8_t *b = p.b + (uint64_t)bn * p.ldb + (uint64_t)k0 * 128;
     uint32_t oa[C::LA], ob[C::LB];
-    const uint32_t chunk = (lane & 3) ^ ((lane >> 4) & 3);
+    bool in_k[2];  // whether the lane's chunk of a cut step is inside k, in even and odd loads
 #pragma unroll
     for (int j = 0; j < C::LA; ++j) {
-        const uint32_t r = (wave * C::LA + j) * 16 + (lane >> 2);
+        const uint32_t r = (wave * C::LA + j) * 8 + (lane >> 3), chunk = (lane & 7) ^ (r >> 1 & 7);
         oa[j] = min(r, p.m - 1 - bm) * (uint32_t)p.lda + chunk * 16;
     }
 #pragma unroll
     for (int j = 0; j < C::LB; ++j) {
-        const uint32_t r = (wave * C::LB + j) * 16 + (lane >> 2);
-        const uint32_t w = r / (C::TN * 16), f = r / 16 % C::TN, i = r % 16;
-        const uint32_t row = w * (C::TN * 16) + i / 4 * (C::TN * 4) + f * 4 + i % 4;
+        const uint32_t r = (wave * C::LB + j) * 8 + (lane >> 3), chunk = (lane & 7) ^ (r >> 1 & 7);
+        const uint32_t row = r / 32 * 32 + column_of<OUT>(r / 16 % 2, r % 16);
         ob[j] = min(row, p.n - 1 - bn) * (uint32_t)p.ldb + chunk * 16;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t chunk = (lane & 7) ^ ((lane >> 4) + 4 * h);
+        in_k[h] = (uint64_t)(k0 + full) * 128 + chunk * 16 < p.k;
     }
     const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) int8_t *)ring;
 
-    const auto fill = [&](uint32_t step, uint32_t slot) {
-        const uint32_t to = lds0 + slot * C::kStage;
-        if (step < full) {
-#pragma unroll
-            for (int j = 0; j < C::LA; ++j) load_to_lds(to + (wave * C::LA + j) * 1024, oa[j], a + (uint64_t)step * 64);
-#pragma unroll
-            for (int j = 0; j < C::LB; ++j)
-                load_to_lds(to + C::BM * 64 + (wave * C::LB + j) * 1024, ob[j], b + (uint64_t)step * 64);
+    // Load j of a step's LA + LB. FAST: the step lies wholly inside k.
+    constexpr int L = C::LA + C::LB;
+    const auto fill = [&](auto fast, int j, uint32_t step, uint32_t slot) {
+        const bool of_a = j < C::LA;
+        const int q = of_a ? j : j - C::LA;
+        const uint32_t nth = wave * (of_a ? C::LA : C::LB) + q;
+        const uint32_t to = lds0 + slot * C::kStage + (of_a ? 0 : C::BM * 128) + nth * 1024;
+        const int8_t *from = (of_a ? a : b) + (uint64_t)step * 128;
+        const uint32_t offset = of_a ? oa[q] : ob[q];
+        if (decltype(fast)::value) {
+            load_to_lds(to, offset, from);
         } else {
-            // the last step, cut by the end of k, and the ring's steps past it: zeros
-            const bool in = step < steps && (uint64_t)(k0 + step) * 64 + chunk * 16 < p.k;
-#pragma unroll
-            for (int j = 0; j < C::LA; ++j)
-                load_to_lds(to + (wave * C::LA + j) * 1024, in ? a + (uint64_t)step * 64 + oa[j] : (const int8_t *)kZeros);
-#pragma unroll
-            for (int j = 0; j < C::LB; ++j)
-                load_to_lds(to + C::BM * 64 + (wave * C::LB + j) * 1024,
-                            in ? b + (uint64_t)step * 64 + ob[j] : (const int8_t *)kZeros);
+            // the step that the end of k cuts, and the ring's steps past it: zeros
+            const bool in = step < full || (step == full && step < steps && (nth & 1 ? in_k[1] : in_k[0]));
+            load_to_lds(to, in ? from + offset : (const int8_t *)kZeros);
         }
     };
 
@@ -144,80 +174,141 @@ __global__ __launch_bounds__(C::NW * 64, 1) void matmul_kernel(MatmulParams p) {
 #pragma unroll
         for (int j = 0; j < C::TM; ++j) acc[i][j] = v4i{0, 0, 0, 0};
 
-    v4i fa[2][C::TM], fb[2][C::TN];
-    const uint32_t at = (lane & 15) * 64 + (((lane >> 4) ^ (lane >> 2)) & 3) * 16;
-    const auto read = [&](uint32_t slot, v4i (&xa)[C::TM], v4i (&xb)[C::TN]) {
-        const int8_t *s = ring + slot * C::kStage + at;
-#pragma unroll
-        for (int i = 0; i < C::TN; ++i) xb[i] = *(const v4i *)(s + C::BM * 64 + (wn * C::TN + i) * 1024);
-#pragma unroll
-        for (int j = 0; j < C::TM; ++j) xa[j] = *(const v4i *)(s + (wm * C::TM + j) * 1024);
-    };
-    const auto multiply = [&](const v4i (&xa)[C::TM], const v4i (&xb)[C::TN]) {
-#pragma unroll
-        for (int j = 0; j < C::TM; ++j)
-#pragma unroll
-            for (int i = 0; i < C::TN; ++i)
-                acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(xb[i], xa[j], acc[i][j], 0, 0, 0);
-    };
+    // Fragments: half h of a step is 64 bytes of k.
+    v4i fa[C::TM], fb[2][C::TN];
+    const uint32_t row = lane & 15, swz = row >> 1;
+    const int8_t *const la = ring + (wm * C::TM * 16 + row) * 128, *const lb = ring + (C::BM + wn * C::TN * 16 + row) * 128;
+    const uint32_t at[2] = {((lane >> 4) ^ swz) * 16, (((lane >> 4) + 4) ^ swz) * 16};
+    const auto read_a = [&](uint32_t slot, int h, int j) { fa[j] = *(const v4i *)(la + slot * C::kStage + at[h] + j * 2048); };
+    const auto read_b = [&](uint32_t slot, int h, int i) { fb[h][i] = *(const v4i *)(lb + slot * C::kStage + at[h] + i * 2048); };
 
-    constexpr int L = C::LA + C::LB;
 #pragma unroll
-    for (int s = 0; s < C::S; ++s) fill(s, s);
-    wait_tiles<(C::S - 1) * L>();
-    read(0, fa[0], fb[0]);
-    // Step i: its fragments are in registers. Wait until step i + 1 has landed for
-    // every wave and every wave has read step i, refill step i's slot, read step
-    // i + 1's fragments under step i's products.
-    uint32_t slot = 0;
-    const auto advance = [&](uint32_t i, int now) {
-        wait_tiles<(C::S - 2) * L>();
-        fill(i + C::S, slot);
-        slot = slot + 1 == C::S ? 0 : slot + 1;
-        read(slot, fa[now ^ 1], fb[now ^ 1]);
-        multiply(fa[now], fb[now]);
-    };
-    uint32_t i = 0;
-    for (; i + 2 <= steps; i += 2) {
-        advance(i, 0);
-        advance(i + 1, 1);
+    for (int s = 0; s < C::S; ++s) {
+        if ((uint32_t)s < full) {
+#pragma unroll
+            for (int j = 0; j < L; ++j) fill(yes{}, j, s, s);
+        } else {
+#pragma unroll
+            for (int j = 0; j < L; ++j) fill(no{}, j, s, s);
+        }
     }
-    if (i < steps) multiply(fa[0], fb[0]);
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load may land after the workgroup's end
+    wait_tiles<(C::S - 1) * L>();
+#pragma unroll
+    for (int i = 0; i < C::TN; ++i) read_b(0, 0, i);
+#pragma unroll
+    for (int j = 0; j < C::TM - 1; ++j) read_a(0, 0, j);
 
+    // A half step's products go by fragments of a: group j is fa[j] times all of fb.
+    // At its start all its fragments but the last of a are in registers (the last
+    // is read behind the first product), and during it those of the next half step
+    // are read: a fragment of a into the registers of the one whose group is done,
+    // those of b into the other set. In the second half of a step the wave waits,
+    // after the first kWait groups, until the next step has landed for every wave
+    // and every wave has read this one; from there on it refills this step's slot.
+    // Reads and loads are dealt between the products, so that the matrix unit
+    // never waits for a run of them.
+    constexpr int kWait = C::TM >= 4 ? C::TM / 4 : 1;
+    uint32_t slot = 0;
+    const auto half = [&](auto fast, auto second, uint32_t step) {
+        constexpr bool kSecond = decltype(second)::value;
+        constexpr int kStart = kSecond ? kWait : 0;            // first group that deals
+        constexpr int kGroups = C::TM - kStart;
+        constexpr int kDeal = kGroups > 1 ? kGroups - 1 : 1;   // the last group reads none of b
+        constexpr int kPerB = (C::TN + kDeal - 1) / kDeal;
+        constexpr int kLoads = kSecond ? L : 0;
+        constexpr int h = kSecond ? 1 : 0;
+        const uint32_t from = kSecond ? (slot + 1 == C::S ? 0 : slot + 1) : slot;
+#pragma unroll
+        for (int j = 0; j < C::TM; ++j) {
+            if (kSecond && j == kWait) {
+                __builtin_amdgcn_sched_barrier(0);
+                wait_tiles<(C::S - 2) * L>();
+            }
+            // the group's share of the work between products: reads of a, of b, loads
+            const int g = j - kStart;
+            const int a0 = g <= 0 ? 0 : j - 1, a1 = g < 0 ? 0 : j;
+            const int b0 = g < 0 ? 0 : min(C::TN, g * kPerB), b1 = g < 0 ? 0 : min(C::TN, (g + 1) * kPerB);
+            const int l0 = g < 0 ? 0 : kLoads * g / kGroups, l1 = g < 0 ? 0 : kLoads * (g + 1) / kGroups;
+            const int na = a1 - a0, nb = b1 - b0, n = na + nb + (l1 - l0);
+#pragma unroll
+            for (int i = 0; i < C::TN; ++i) {
+                multiply_add(acc[i][j], fb[h][i], fa[j]);
+                if (j == 0 && i == 0) read_a(slot, h, C::TM - 1);
+#pragma unroll
+                for (int x = 0; x < n; ++x) {
+                    if (x * C::TN / n != i) continue;
+                    if (x < na) read_a(from, h ^ 1, a0 + x);
+                    else if (x < na + nb) read_b(from, h ^ 1, b0 + x - na);
+                    else fill(fast, l0 + x - na - nb, step + C::S, slot);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+        if (kSecond) slot = from;
+    };
+    uint32_t step = 0;
+    for (; step + C::S < full; ++step) {
+        half(yes{}, no{}, step);
+        half(yes{}, yes{}, step);
+    }
+    for (; step < steps; ++step) {
+        half(no{}, no{}, step);
+        half(no{}, yes{}, step);
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load may land after the workgroup's end
+    settle();
+#pragma unroll
+    for (int i = 0; i < C::TN; ++i)
+#pragma unroll
+        for (int j = 0; j < C::TM; ++j) settled(acc[i][j]);
+
+    // Epilogue: kCols columns of a lane at a time (16 bytes of y).
+    constexpr int kCols = sizeof(OUT) == 4 ? 4 : 8, kFrags = kCols / 4;
     const uint32_t m0 = bm + wm * C::TM * 16 + (lane & 15);
-    const uint32_t n0 = bn + wn * C::TN * 16 + (lane >> 4) * (C::TN * 4);
-    if (n0 >= p.n) return;
-    const uint32_t there = min((uint32_t)(C::TN * 4), p.n - n0);
+    const bool split = sizeof(OUT) == 4 && p.part;
+    float sa[C::TM];
 #pragma unroll
-    for (int j = 0; j < C::TM; ++j) {
-        const uint32_t m = m0 + j * 16;
-        if (m >= p.m) continue;
-        if (sizeof(OUT) == 4 && p.part) {
-            int32_t *out = p.part + ((uint64_t)blockIdx.y * p.m + m) * p.n + n0;
+    for (int j = 0; j < C::TM; ++j) sa[j] = split ? 0.0f : p.sa[min(m0 + j * 16, p.m - 1)];
 #pragma unroll
-            for (int c = 0; c < C::TN; ++c) {
-                if (4 * c + 4 <= (int)there) __builtin_memcpy(out + 4 * c, &acc[c][j], 16);
+    for (int f = 0; f < C::TN; f += kFrags) {
+        const uint32_t n0 = bn + (wn * C::TN + f / 2 * 2) * 16 + column_of<OUT>(f & 1, lane >> 4 << 2);
+        if (n0 >= p.n) continue;
+        const int there = (int)min((uint32_t)kCols, p.n - n0);
+        if (split) {
+#pragma unroll
+            for (int j = 0; j < C::TM; ++j) {
+                if (m0 + j * 16 >= p.m) continue;
+                int32_t *out = p.part + ((uint64_t)blockIdx.y * p.m + m0 + j * 16) * p.n + n0;
+                if (there == kCols) __builtin_memcpy(out, &acc[f][j], 16);
                 else
                     for (int e = 0; e < 4; ++e)
-                        if (4 * c + e < (int)there) out[4 * c + e] = acc[c][j][e];
+                        if (e < there) out[e] = acc[f][j][e];
             }
             continue;
         }
-        const float sa = p.sa[m];
-        OUT *out = (OUT *)p.y + (uint64_t)m * p.ldy + n0;
+        float sb[kCols], bias[kCols];
 #pragma unroll
-        for (int c = 0; c < C::TN; ++c) {
-            if (4 * c + 4 <= (int)there) {
-                OUT v[4];
+        for (int e = 0; e < kCols; ++e) {
+            const uint32_t col = min(n0 + e, p.n - 1);
+            sb[e] = p.sb ? p.sb[col] : 1.0f;
+            bias[e] = p.bias ? p.bias[col] : 0.0f;
+        }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = (OUT)finish((float)acc[c][j][e], sa, p.sb, p.bias, n0 + 4 * c + e);
-                __builtin_memcpy(out + 4 * c, v, sizeof(v));
-            } else {
-                for (int e = 0; e < 4; ++e)
-                    if (4 * c + e < (int)there)
-                        out[4 * c + e] = (OUT)finish((float)acc[c][j][e], sa, p.sb, p.bias, n0 + 4 * c + e);
+        for (int j = 0; j < C::TM; ++j) {
+            if (m0 + j * 16 >= p.m) continue;
+            OUT v[kCols];
+#pragma unroll
+            for (int e = 0; e < kCols; ++e) {
+                float x = (float)acc[f + e / 4][j][e % 4] * sa[j] * sb[e];
+                if (p.bias) x += bias[e];  // adding 0 would turn -0 into 0
+                v[e] = (OUT)x;
             }
+            OUT *out = (OUT *)p.y + (uint64_t)(m0 + j * 16) * p.ldy + n0;
+            if (there == kCols) __builtin_memcpy(out, v, sizeof(v));
+            else
+#pragma unroll
+                for (int e = 0; e < kCols; ++e)
+                    if (e < there) out[e] = v[e];
         }
     }
 }
