@@ -138,7 +138,12 @@ Plan plan_matmul(bool a_aligned, uint64_t lda, bool a_padded, bool b_aligned, ui
 
 template <class C, class OUT>
 void launch_tiles(const MatmulParams &p, hipStream_t stream) {
-    matmul_kernel<C, OUT><<<dim3(p.tiles_m * p.tiles_n, p.splits), C::NW * 64, 0, stream>>>(p);
+    MatmulParams q = p;
+    const uint32_t tiles = p.tiles_m * p.tiles_n;
+    // a tile that fills a CU: one workgroup a CU goes from tile to tile
+    const bool stay = C::kLds > 80 * 1024 && tiles > kCus && p.steps_per_split >= C::S && p.splits == 1;
+    q.stride = stay ? kCus / 8 : tiles;
+    matmul_kernel<C, OUT><<<dim3(stay ? (uint32_t)kCus : tiles, p.splits), C::NW * 64, 0, stream>>>(q);
 }
 
 template <class OUT>

@@ -22,10 +22,12 @@ struct MatmulParams {
     uint32_t m, n, k;
     uint32_t tiles_m, tiles_n;
     uint32_t splits, steps_per_split;  // 128-byte steps of k
+    uint32_t stride;  // tiles of an XCD's run that a workgroup goes on by: it takes every stride-th
 };
 
 // Sixteen zero bytes that tile loads past the end of k are pointed at.
 static __device__ __align__(16) const uint32_t kZeros[4] = {0, 0, 0, 0};
+static __device__ const float kOne = 1.0f, kMinusZero = -0.0f;  // a scale and a bias that change nothing
 
 // The epilogue, one rounding at a time.
 __device__ __forceinline__ float finish(float acc, float sa, const float *sb, const float *bias, uint32_t col) {
@@ -49,6 +51,12 @@ __device__ __forceinline__ void load_to_lds(uint32_t lds, const int8_t *from) {
                  :: "s"(lds), "v"(from) : "memory");
 }
 
+// The same with 4 bytes a lane.
+__device__ __forceinline__ void load_word_to_lds(uint32_t lds, const float *from) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
+                 :: "s"(lds), "v"(from) : "memory");
+}
+
 // Tiles of BM rows of a and BN rows of b. A step is 128 bytes of k: a cache line of
 // each row, so that every request to the L2 is a whole line (steps of 64 bytes made
 // nearly twice the requests and were bound by them). LDS holds a ring of S steps,
@@ -66,7 +74,9 @@ struct Tile {
     static constexpr int NW = WM * WN;
     static constexpr int LA = BM / 8 / NW, LB = BN / 8 / NW;  // loads a wave and step
     static constexpr int kStage = (BM + BN) * 128;
-    static constexpr int kLds = S * kStage;
+    // two sets of a wave's scales: a row's, a column's, its bias
+    static constexpr int kScales = (TM * 16 + 2 * TN * 16) * 4;
+    static constexpr int kLds = S * kStage + 2 * NW * kScales;
     static_assert(LA * 8 * NW == BM && LB * 8 * NW == BN && kLds <= 160 * 1024, "");
 };
 
@@ -86,6 +96,7 @@ __device__ __forceinline__ void multiply_add(v4i &acc, const v4i &b, const v4i &
     asm("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(acc) : "v"(b), "v"(a));
 }
 __device__ __forceinline__ void settle() { asm volatile("s_nop 15\n\ts_nop 7" ::: "memory"); }
+__device__ __forceinline__ void start() { asm volatile("s_nop 3"); }  // between writing accumulators and a product
 __device__ __forceinline__ void settled(v4i &acc) { asm volatile("" : "+a"(acc)); }
 
 // The column of y, within 32, that row i of b's fragment f (of a pair) belongs to.
@@ -115,64 +126,76 @@ __global__ __launch_bounds__(C::NW * 64, 1) void matmul_kernel(MatmulParams p) {
     // tiles, in bands of 8 tile rows, so that the tiles an XCD works on together
     // share their rows of a and b in its L2.
     const uint32_t tiles = p.tiles_m * p.tiles_n;
-    const uint32_t xcd = blockIdx.x % 8, nth = blockIdx.x / 8;
-    const uint32_t id = xcd * (tiles / 8) + min(xcd, tiles % 8) + nth;
-    const uint32_t band = id / (8 * p.tiles_n), in_band = id % (8 * p.tiles_n);
-    const uint32_t band_rows = min(8u, p.tiles_m - band * 8);
-    const uint32_t bm = (band * 8 + in_band % band_rows) * C::BM, bn = in_band / band_rows * C::BN;
+    const uint32_t xcd = blockIdx.x % 8;
+    const uint32_t run = tiles / 8 + (xcd < tiles % 8), first = xcd * (tiles / 8) + min(xcd, tiles % 8);
+    uint32_t nth = blockIdx.x / 8;
+    if (nth >= run) return;
 
     const uint32_t k0 = blockIdx.y * p.steps_per_split;  // first step
     const uint32_t all = (p.k + 127) / 128;
     const uint32_t steps = min(p.steps_per_split, all - k0);
     const uint32_t full = min(steps, p.k / 128 - min(p.k / 128, k0));  // steps wholly inside k
 
-    // This lane's part of the wave's loads: eight lanes a row. Rows past the end
-    // repeat the last one.
-    const int8_t *a = p.a + (uint64_t)bm * p.lda + (uint64_t)k0 * 128;
-    const int8_t *b = p.b + (uint64_t)bn * p.ldb + (uint64_t)k0 * 128;
-    uint32_t oa[C::LA], ob[C::LB];
-    bool in_k[2];  // whether the lane's chunk of a cut step is inside k, in even and odd loads
-#pragma unroll
-    for (int j = 0; j < C::LA; ++j) {
-        const uint32_t r = (wave * C::LA + j) * 8 + (lane >> 3), chunk = (lane & 7) ^ (r >> 1 & 7);
-        oa[j] = min(r, p.m - 1 - bm) * (uint32_t)p.lda + chunk * 16;
-    }
-#pragma unroll
-    for (int j = 0; j < C::LB; ++j) {
-        const uint32_t r = (wave * C::LB + j) * 8 + (lane >> 3), chunk = (lane & 7) ^ (r >> 1 & 7);
-        const uint32_t row = r / 32 * 32 + column_of<OUT>(r / 16 % 2, r % 16);
-        ob[j] = min(row, p.n - 1 - bn) * (uint32_t)p.ldb + chunk * 16;
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const uint32_t chunk = (lane & 7) ^ ((lane >> 4) + 4 * h);
-        in_k[h] = (uint64_t)(k0 + full) * 128 + chunk * 16 < p.k;
-    }
+    // The tile that is being loaded: this lane's part of the wave's loads, eight
+    // lanes a row. Rows past the end repeat the last one.
     const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) int8_t *)ring;
+    uint32_t load_m, load_n;
+    const int8_t *a, *b;
+    uint32_t oa[C::LA], ob[C::LB];
+    const auto place = [&](uint32_t id, uint32_t set) __attribute__((always_inline)) {
+        const uint32_t band = id / (8 * p.tiles_n), in_band = id % (8 * p.tiles_n);
+        const uint32_t band_rows = min(8u, p.tiles_m - band * 8);
+        load_m = (band * 8 + in_band % band_rows) * C::BM;
+        load_n = in_band / band_rows * C::BN;
+        a = p.a + (uint64_t)load_m * p.lda + (uint64_t)k0 * 128;
+        b = p.b + (uint64_t)load_n * p.ldb + (uint64_t)k0 * 128;
+#pragma unroll
+        for (int j = 0; j < C::LA; ++j) {
+            const uint32_t r = (wave * C::LA + j) * 8 + (lane >> 3), chunk = (lane & 7) ^ (r >> 1 & 7);
+            oa[j] = min(r, p.m - 1 - load_m) * (uint32_t)p.lda + chunk * 16;
+        }
+#pragma unroll
+        for (int j = 0; j < C::LB; ++j) {
+            const uint32_t r = (wave * C::LB + j) * 8 + (lane >> 3), chunk = (lane & 7) ^ (r >> 1 & 7);
+            const uint32_t row = r / 32 * 32 + column_of<OUT>(r / 16 % 2, r % 16);
+            ob[j] = min(row, p.n - 1 - load_n) * (uint32_t)p.ldb + chunk * 16;
+        }
+        // its scales, before its first step: they have landed when that has
+        const uint32_t to = lds0 + C::S * C::kStage + (set * C::NW + wave) * C::kScales;
+#pragma unroll
+        for (int i = 0; i < (C::TM * 16 + 63) / 64; ++i)
+            if (C::TM >= 4 || lane < C::TM * 16)
+                load_word_to_lds(to + i * 256, p.sa + min(load_m + wm * C::TM * 16 + i * 64 + lane, p.m - 1));
+#pragma unroll
+        for (int i = 0; i < (C::TN * 16 + 63) / 64; ++i) {
+            const uint32_t col = min(load_n + wn * C::TN * 16 + i * 64 + lane, p.n - 1);
+            if (C::TN < 4 && lane >= C::TN * 16) continue;
+            load_word_to_lds(to + C::TM * 64 + i * 256, p.sb ? p.sb + col : &kOne);
+            load_word_to_lds(to + C::TM * 64 + C::TN * 64 + i * 256, p.bias ? p.bias + col : &kMinusZero);
+        }
+    };
+    // where the lane's chunk of a step begins, in even and odd loads
+    const uint32_t chunk0 = ((lane & 7) ^ (lane >> 4)) * 16, chunk1 = chunk0 ^ 64;
 
     // Load j of a step's LA + LB. FAST: the step lies wholly inside k.
     constexpr int L = C::LA + C::LB;
-    const auto fill = [&](auto fast, int j, uint32_t step, uint32_t slot) {
+    const auto fill = [&](auto fast, int j, uint32_t step, uint32_t slot) __attribute__((always_inline)) {
         const bool of_a = j < C::LA;
         const int q = of_a ? j : j - C::LA;
-        const uint32_t nth = wave * (of_a ? C::LA : C::LB) + q;
-        const uint32_t to = lds0 + slot * C::kStage + (of_a ? 0 : C::BM * 128) + nth * 1024;
+        const uint32_t part = wave * (of_a ? C::LA : C::LB) + q;
+        const uint32_t to = lds0 + slot * C::kStage + (of_a ? 0 : C::BM * 128) + part * 1024;
         const int8_t *from = (of_a ? a : b) + (uint64_t)step * 128;
         const uint32_t offset = of_a ? oa[q] : ob[q];
         if (decltype(fast)::value) {
             load_to_lds(to, offset, from);
         } else {
             // the step that the end of k cuts, and the ring's steps past it: zeros
-            const bool in = step < full || (step == full && step < steps && (nth & 1 ? in_k[1] : in_k[0]));
-            load_to_lds(to, in ? from + offset : (const int8_t *)kZeros);
+            const uint32_t inside = step < full ? 128u : step < steps ? p.k % 128 : 0u;
+            load_to_lds(to, (part & 1 ? chunk1 : chunk0) < inside ? from + offset : (const int8_t *)kZeros);
         }
     };
 
     v4i acc[C::TN][C::TM];
-#pragma unroll
-    for (int i = 0; i < C::TN; ++i)
-#pragma unroll
-        for (int j = 0; j < C::TM; ++j) acc[i][j] = v4i{0, 0, 0, 0};
 
     // Fragments: half h of a step is 64 bytes of k.
     v4i fa[C::TM], fb[2][C::TN];
@@ -182,6 +205,7 @@ __global__ __launch_bounds__(C::NW * 64, 1) void matmul_kernel(MatmulParams p) {
     const auto read_a = [&](uint32_t slot, int h, int j) { fa[j] = *(const v4i *)(la + slot * C::kStage + at[h] + j * 2048); };
     const auto read_b = [&](uint32_t slot, int h, int i) { fb[h][i] = *(const v4i *)(lb + slot * C::kStage + at[h] + i * 2048); };
 
+    place(first + nth, 0);
 #pragma unroll
     for (int s = 0; s < C::S; ++s) {
         if ((uint32_t)s < full) {
@@ -204,12 +228,13 @@ __global__ __launch_bounds__(C::NW * 64, 1) void matmul_kernel(MatmulParams p) {
     // are read: a fragment of a into the registers of the one whose group is done,
     // those of b into the other set. In the second half of a step the wave waits,
     // after the first kWait groups, until the next step has landed for every wave
-    // and every wave has read this one; from there on it refills this step's slot.
+    // and every wave has read this one; from there on it refills this step's slot
+    // with step `later`.
     // Reads and loads are dealt between the products, so that the matrix unit
     // never waits for a run of them.
     constexpr int kWait = C::TM >= 4 ? C::TM / 4 : 1;
     uint32_t slot = 0;
-    const auto half = [&](auto fast, auto second, uint32_t step) {
+    const auto half = [&](auto fast, auto second, uint32_t later) __attribute__((always_inline)) {
         constexpr bool kSecond = decltype(second)::value;
         constexpr int kStart = kSecond ? kWait : 0;            // first group that deals
         constexpr int kGroups = C::TM - kStart;
@@ -233,84 +258,119 @@ __global__ __launch_bounds__(C::NW * 64, 1) void matmul_kernel(MatmulParams p) {
 #pragma unroll
             for (int i = 0; i < C::TN; ++i) {
                 multiply_add(acc[i][j], fb[h][i], fa[j]);
-                if (j == 0 && i == 0) read_a(slot, h, C::TM - 1);
+                if (j == 0 && i == 0) {
+                    __builtin_amdgcn_sched_barrier(0);  // the product waits for all reads so far
+                    read_a(slot, h, C::TM - 1);
+                }
 #pragma unroll
                 for (int x = 0; x < n; ++x) {
                     if (x * C::TN / n != i) continue;
                     if (x < na) read_a(from, h ^ 1, a0 + x);
                     else if (x < na + nb) read_b(from, h ^ 1, b0 + x - na);
-                    else fill(fast, l0 + x - na - nb, step + C::S, slot);
+                    else fill(fast, l0 + x - na - nb, later, slot);
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
         if (kSecond) slot = from;
     };
-    uint32_t step = 0;
-    for (; step + C::S < full; ++step) {
-        half(yes{}, no{}, step);
-        half(yes{}, yes{}, step);
-    }
-    for (; step < steps; ++step) {
-        half(no{}, no{}, step);
-        half(no{}, yes{}, step);
-    }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load may land after the workgroup's end
-    settle();
+    const int fast_steps = __builtin_amdgcn_readfirstlane(max(0, (int)full - C::S));
+    // Tile after tile: the last S steps of one load the first S of the next, which
+    // land during its epilogue.
+    for (uint32_t set = 0;; set ^= 1) {
+        const uint32_t bm = load_m, bn = load_n;
 #pragma unroll
-    for (int i = 0; i < C::TN; ++i)
+        for (int i = 0; i < C::TN; ++i)
 #pragma unroll
-        for (int j = 0; j < C::TM; ++j) settled(acc[i][j]);
+            for (int j = 0; j < C::TM; ++j) acc[i][j] = v4i{0, 0, 0, 0};
+        start();
+        bool more = false;
+        int step = 0;
+        for (int left = fast_steps; left > 0; --left, ++step) {
+            half(yes{}, no{}, step + C::S);
+            half(yes{}, yes{}, step + C::S);
+        }
+        for (int left = (int)steps - step; left > 0; --left, ++step) {
+            uint32_t later = step + C::S;
+            if (later >= steps) {
+                if (later == steps && nth + p.stride < run) {
+                    more = true;
+                    nth += p.stride;
+                    place(first + nth, set ^ 1);
+                }
+                later = more ? later - steps : steps;  // past the last tile: zeros
+            }
+            half(no{}, no{}, later);
+            half(no{}, yes{}, later);
+        }
+        settle();
+#pragma unroll
+        for (int i = 0; i < C::TN; ++i)
+#pragma unroll
+            for (int j = 0; j < C::TM; ++j) settled(acc[i][j]);
 
-    // Epilogue: kCols columns of a lane at a time (16 bytes of y).
-    constexpr int kCols = sizeof(OUT) == 4 ? 4 : 8, kFrags = kCols / 4;
-    const uint32_t m0 = bm + wm * C::TM * 16 + (lane & 15);
-    const bool split = sizeof(OUT) == 4 && p.part;
-    float sa[C::TM];
+        // Epilogue: kCols columns of a lane at a time (16 bytes of y). A tile wholly
+        // inside y goes without tests between its stores.
+        const float *scales = (const float *)(ring + C::S * C::kStage + (set * C::NW + wave) * C::kScales);
+        const uint32_t m0 = bm + wm * C::TM * 16 + row;
+        float sa[C::TM];
 #pragma unroll
-    for (int j = 0; j < C::TM; ++j) sa[j] = split ? 0.0f : p.sa[min(m0 + j * 16, p.m - 1)];
+        for (int j = 0; j < C::TM; ++j) sa[j] = scales[j * 16 + row];
+        const auto write = [&](auto inside) __attribute__((always_inline)) {
+            constexpr bool kInside = decltype(inside)::value;
+            constexpr int kCols = sizeof(OUT) == 4 ? 4 : 8, kFrags = kCols / 4;
+            OUT *const y0 = (OUT *)p.y + (uint64_t)m0 * p.ldy + bn + wn * C::TN * 16;
+            const uint64_t down = p.ldy * 16;
 #pragma unroll
-    for (int f = 0; f < C::TN; f += kFrags) {
-        const uint32_t n0 = bn + (wn * C::TN + f / 2 * 2) * 16 + column_of<OUT>(f & 1, lane >> 4 << 2);
-        if (n0 >= p.n) continue;
-        const int there = (int)min((uint32_t)kCols, p.n - n0);
-        if (split) {
+            for (int f = 0; f < C::TN; f += kFrags) {
+                const uint32_t at_n = f / 2 * 32 + column_of<OUT>(f & 1, lane >> 4 << 2);
+                const uint32_t n0 = bn + wn * C::TN * 16 + at_n;
+                if (!kInside && n0 >= p.n) continue;
+                const int there = kInside ? kCols : (int)min((uint32_t)kCols, p.n - n0);
+                float sb[kCols], bias[kCols];
+#pragma unroll
+                for (int e = 0; e < kCols; ++e) {
+                    sb[e] = scales[C::TM * 16 + at_n + e];
+                    bias[e] = scales[C::TM * 16 + C::TN * 16 + at_n + e];
+                }
+                OUT *out = y0 + at_n;
+#pragma unroll
+                for (int j = 0; j < C::TM; ++j, out += down) {
+                    if (!kInside && m0 + j * 16 >= p.m) continue;
+                    OUT v[kCols];
+#pragma unroll
+                    for (int e = 0; e < kCols; ++e)
+                        v[e] = (OUT)((float)acc[f + e / 4][j][e % 4] * sa[j] * sb[e] + bias[e]);
+                    if (there == kCols) __builtin_memcpy(out, v, sizeof(v));
+                    else
+#pragma unroll
+                        for (int e = 0; e < kCols; ++e)
+                            if (e < there) out[e] = v[e];
+                }
+            }
+        };
+        const auto write_part = [&]() __attribute__((always_inline)) {
 #pragma unroll
             for (int j = 0; j < C::TM; ++j) {
                 if (m0 + j * 16 >= p.m) continue;
-                int32_t *out = p.part + ((uint64_t)blockIdx.y * p.m + m0 + j * 16) * p.n + n0;
-                if (there == kCols) __builtin_memcpy(out, &acc[f][j], 16);
-                else
-                    for (int e = 0; e < 4; ++e)
-                        if (e < there) out[e] = acc[f][j][e];
+#pragma unroll
+                for (int f = 0; f < C::TN; ++f) {
+                    const uint32_t n0 = bn + (wn * C::TN + f) * 16 + (lane >> 4) * 4;
+                    if (n0 >= p.n) continue;
+                    int32_t *out = p.part + ((uint64_t)blockIdx.y * p.m + m0 + j * 16) * p.n + n0;
+                    if (n0 + 4 <= p.n) __builtin_memcpy(out, &acc[f][j], 16);
+                    else
+                        for (int e = 0; e < 4; ++e)
+                            if (n0 + e < p.n) out[e] = acc[f][j][e];
+                }
             }
-            continue;
-        }
-        float sb[kCols], bias[kCols];
-#pragma unroll
-        for (int e = 0; e < kCols; ++e) {
-            const uint32_t col = min(n0 + e, p.n - 1);
-            sb[e] = p.sb ? p.sb[col] : 1.0f;
-            bias[e] = p.bias ? p.bias[col] : 0.0f;
-        }
-#pragma unroll
-        for (int j = 0; j < C::TM; ++j) {
-            if (m0 + j * 16 >= p.m) continue;
-            OUT v[kCols];
-#pragma unroll
-            for (int e = 0; e < kCols; ++e) {
-                float x = (float)acc[f + e / 4][j][e % 4] * sa[j] * sb[e];
-                if (p.bias) x += bias[e];  // adding 0 would turn -0 into 0
-                v[e] = (OUT)x;
-            }
-            OUT *out = (OUT *)p.y + (uint64_t)(m0 + j * 16) * p.ldy + n0;
-            if (there == kCols) __builtin_memcpy(out, v, sizeof(v));
-            else
-#pragma unroll
-                for (int e = 0; e < kCols; ++e)
-                    if (e < there) out[e] = v[e];
-        }
+        };
+        if (sizeof(OUT) == 4 && p.part) write_part();
+        else if (bm + C::BM <= p.m && bn + C::BN <= p.n) write(yes{});
+        else write(no{});
+        if (!more) break;
     }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load may land after the workgroup's end
 }
 
 // Joins the parts of a split sum: exact in 64 bits, then the epilogue.
