@@ -60,52 +60,79 @@ __device__ __forceinline__ Pair join(Pair a, Pair b, float c) {
     return {m, a.s * exp_scaled(a.m, base, c) + b.s * exp_scaled(b.m, base, c)};
 }
 
-template <class F>
-__device__ __forceinline__ float block_reduce(float v, float none, float *lds, F f) {
-#pragma unroll
-    for (int o = 32; o; o >>= 1) v = f(v, __shfl_xor(v, o));
+// A wave's pair: the maximum, then the sums relative to it.
+__device__ __forceinline__ Pair wave_join(Pair v, float c) {
+    const float m = wave_max(v.m), base = base_of(m);
+    return {m, wave_sum(v.s * exp_scaled(v.m, base, c))};
+}
+
+// Over the workgroup: the waves' results meet in `lds` (a word a wave and value) and
+// every wave reduces them again.
+__device__ __forceinline__ float block_sum(float v, float *lds) {
+    v = wave_sum(v);
     __syncthreads();  // lds may still be read from the last call
     if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
     __syncthreads();
-    v = none;
-    const int waves = blockDim.x >> 6;
-    for (int w = 0; w < waves; ++w) v = f(v, lds[w]);
-    return v;
-}
-__device__ __forceinline__ float block_sum(float v, float *lds) {
-    return block_reduce(v, 0.0f, lds, [](float a, float b) { return a + b; });
+    const uint32_t lane = threadIdx.x & 63;
+    return wave_sum(lane < blockDim.x / 64 ? lds[lane] : 0.0f);
 }
 __device__ __forceinline__ float block_max(float v, float *lds) {
-    return block_reduce(v, -INFINITY, lds, [](float a, float b) { return fmaxf(a, b); });
+    v = wave_max(v);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+    __syncthreads();
+    const uint32_t lane = threadIdx.x & 63;
+    return wave_max(lane < blockDim.x / 64 ? lds[lane] : -INFINITY);
 }
-
 __device__ __forceinline__ Pair block_join(Pair v, float c, float *lds) {
-#pragma unroll
-    for (int o = 32; o; o >>= 1) v = join(v, Pair{__shfl_xor(v.m, o), __shfl_xor(v.s, o)}, c);
+    v = wave_join(v, c);
     __syncthreads();
     if ((threadIdx.x & 63) == 0) {
-        lds[threadIdx.x >> 5] = v.m;
-        lds[(threadIdx.x >> 5) + 1] = v.s;
+        lds[threadIdx.x >> 6] = v.m;
+        lds[16 + (threadIdx.x >> 6)] = v.s;
     }
     __syncthreads();
-    v = {-INFINITY, 0.0f};
-    const int waves = blockDim.x >> 6;
-    for (int w = 0; w < waves; ++w) v = join(v, Pair{lds[2 * w], lds[2 * w + 1]}, c);
-    return v;
+    const uint32_t lane = threadIdx.x & 63;
+    const bool in = lane < blockDim.x / 64;
+    return wave_join({in ? lds[lane] : -INFINITY, in ? lds[16 + lane] : 0.0f}, c);
 }
 
-__device__ __forceinline__ int64_t read_index(const void *p, uint32_t type, uint64_t at) {
-    return type == QSGD_I64 ? ((const int64_t *)p)[at] : ((const int32_t *)p)[at];
+// An entry as it lies in memory. The loads do not depend on the types, so that they
+// can be issued ahead of a row's logits and looked at later.
+struct RawEntry {
+    uint32_t i0, i1;  // the index's words
+    uint32_t t0, t1;  // the logit's halves
+};
+static __device__ const uint64_t kNoEntry = 0;  // where entry 0 of calls without entries is read
+__device__ __forceinline__ RawEntry load_entry(const DistillParams &p, uint32_t row, uint32_t i) {
+    const bool wide_i = p.itype == QSGD_I64, wide_t = p.ttype == QSGD_F32;
+    typedef const __attribute__((address_space(1))) char *Global;  // or the choice would make generic loads of them
+    const Global none = (Global)&kNoEntry;
+    const Global at = p.k ? (Global)p.idx + (((uint64_t)row * p.ldi + i) << (wide_i ? 3 : 2)) : none;
+    const Global t = p.k ? (Global)p.t + (((uint64_t)row * p.ldt + i) << (wide_t ? 2 : 1)) : none;
+    typedef const __attribute__((address_space(1))) uint32_t *Word;
+    typedef const __attribute__((address_space(1))) uint16_t *Half;
+    return {*(Word)at, *(Word)(at + (wide_i ? 4 : 0)), *(Half)t, *(Half)(t + (wide_t ? 2 : 0))};
 }
-__device__ __forceinline__ float read_logit(const void *p, uint32_t type, uint64_t at) {
-    return type == QSGD_F32 ? ((const float *)p)[at]
-                            : type == QSGD_F16 ? (float)((const f16 *)p)[at] : (float)((const bf16 *)p)[at];
+// Its index, -1 where it is none.
+__device__ __forceinline__ int entry_index(const DistillParams &p, const RawEntry &r) {
+    const bool high = p.itype == QSGD_I64 ? r.i1 != 0 : (int32_t)r.i0 < 0;
+    return high || r.i0 >= p.vocab ? -1 : (int)r.i0;
+}
+__device__ __forceinline__ float entry_logit(const DistillParams &p, const RawEntry &r) {
+    if (p.ttype == QSGD_F32) return __uint_as_float(r.t0 | r.t1 << 16);
+    if (p.ttype == QSGD_BF16) return __uint_as_float(r.t0 << 16);
+    const uint16_t h = (uint16_t)r.t0;
+    f16 v;
+    __builtin_memcpy(&v, &h, 2);
+    return (float)v;
 }
 
 // A row's entries in LDS, and what the teacher says of them.
 struct Entries {
     int at[kMaxEntries];    // index in the vocabulary, -1: no entry
     float z[kMaxEntries];   // student's logit
+    float t[kMaxEntries];   // teacher's logit / tau
     float p[kMaxEntries];   // teacher's probability
     float red[2 * 16];
 };
@@ -116,20 +143,21 @@ struct TeacherSums {
     float rest;     // p_r
 };
 
-// Reads a row's entries (by the whole workgroup; ends with a barrier).
+// Reads a row's entries (by the whole workgroup; ends with a barrier). `ahead` is
+// this thread's first one, loaded before.
 template <class T>
-__device__ __forceinline__ TeacherSums read_entries(const DistillParams &p, uint32_t row, Entries &e) {
+__device__ __forceinline__ TeacherSums read_entries(const DistillParams &p, uint32_t row, Entries &e, RawEntry ahead) {
     const T *z = (const T *)p.z + (uint64_t)row * p.ldz;
     float top = -INFINITY, some = 0.0f;
     for (uint32_t i = threadIdx.x; i < p.k; i += blockDim.x) {
-        const int64_t at = read_index(p.idx, p.itype, (uint64_t)row * p.ldi + i);
-        const bool there = at >= 0 && at < (int64_t)p.vocab;
-        e.at[i] = there ? (int)at : -1;
-        e.z[i] = there ? (float)z[at] : -INFINITY;
-        const float x = there ? read_logit(p.t, p.ttype, (uint64_t)row * p.ldt + i) * p.inv_tau : -INFINITY;
-        e.p[i] = x;
+        const RawEntry r = i < blockDim.x ? ahead : load_entry(p, row, i);
+        const int at = entry_index(p, r);
+        const float x = at >= 0 ? entry_logit(p, r) * p.inv_tau : -INFINITY;
+        e.at[i] = at;
+        e.z[i] = at >= 0 ? (float)z[at] : -INFINITY;
+        e.t[i] = x;
         top = fmaxf(top, x);
-        some = there ? 1.0f : some;
+        some = at >= 0 ? 1.0f : some;
     }
     TeacherSums s;
     s.some = block_max(some, e.red) > 0.0f;
@@ -137,7 +165,7 @@ __device__ __forceinline__ TeacherSums read_entries(const DistillParams &p, uint
     if (p.teacher_lse) {
         s.shift = p.teacher_lse[row];
         for (uint32_t i = threadIdx.x; i < p.k; i += blockDim.x) {
-            const float v = e.at[i] >= 0 ? expf(e.p[i] - s.shift) : 0.0f;
+            const float v = e.at[i] >= 0 ? expf(e.t[i] - s.shift) : 0.0f;
             e.p[i] = v;
             sum += v;
         }
@@ -146,7 +174,7 @@ __device__ __forceinline__ TeacherSums read_entries(const DistillParams &p, uint
     } else {
         top = base_of(block_max(top, e.red));
         for (uint32_t i = threadIdx.x; i < p.k; i += blockDim.x) {
-            const float v = e.at[i] >= 0 ? expf(e.p[i] - top) : 0.0f;
+            const float v = e.at[i] >= 0 ? expf(e.t[i] - top) : 0.0f;
             e.p[i] = v;
             sum += v;
         }
@@ -158,6 +186,10 @@ __device__ __forceinline__ TeacherSums read_entries(const DistillParams &p, uint
     }
     __syncthreads();
     return s;
+}
+
+__device__ __forceinline__ RawEntry first_entry(const DistillParams &p, uint32_t row) {
+    return threadIdx.x < p.k ? load_entry(p, row, threadIdx.x) : RawEntry{};
 }
 
 // The bits of the entries inside a segment [lo, lo + n); ends with a barrier.
@@ -211,6 +243,12 @@ struct Stats {
 
 __device__ __forceinline__ float inverse(float s) { return s == 0.0f ? 0.0f : 1.0f / s; }
 
+// The remainder's term of the loss.
+__device__ __forceinline__ float rest_loss(const DistillParams &p, const TeacherSums &ts, Pair rest, float base, float log_sum) {
+    if (!p.teacher_lse || ts.rest == 0.0f || rest.s == 0.0f) return 0.0f;
+    return ts.rest * (logf(ts.rest) - ((base_of(rest.m) - base) * p.inv_tau + logf(rest.s) - log_sum));
+}
+
 __device__ __forceinline__ Stats finish_row(const DistillParams &p, uint32_t row, const TeacherSums &ts, Pair scanned,
                                             Entries &e) {
     const float c = kLog2e * p.inv_tau;
@@ -225,15 +263,43 @@ __device__ __forceinline__ Stats finish_row(const DistillParams &p, uint32_t row
     for (uint32_t i = threadIdx.x; i < p.k; i += blockDim.x) {
         const float pi = e.p[i];
         if (e.at[i] < 0 || pi == 0.0f) continue;
-        const float log_p = read_logit(p.t, p.ttype, (uint64_t)row * p.ldt + i) * p.inv_tau - ts.shift;
+        const float log_p = e.t[i] - ts.shift;
         const float log_q = all.s == 0.0f ? -INFINITY : (e.z[i] - base) * p.inv_tau - log_sum;
         loss += pi * (log_p - log_q);
     }
     loss = block_sum(loss, e.red);
-    if (p.teacher_lse && ts.rest != 0.0f && scanned.s != 0.0f)
-        loss += ts.rest * (logf(ts.rest) - ((base_of(scanned.m) - base) * p.inv_tau + logf(scanned.s) - log_sum));
+    loss += rest_loss(p, ts, scanned, base, log_sum);
     if (threadIdx.x == 0 && p.loss) p.loss[row] = ts.some ? loss : 0.0f;
     return {all.m, inverse(all.s), scanned.m, inverse(scanned.s)};
+}
+
+// What the gradients of a row share.
+struct GradientRow {
+    float g, factor, base;  // g / tau; that of e_j; m_r
+    bool none;              // the row has no gradient
+};
+__device__ __forceinline__ GradientRow gradient_row(const DistillParams &p, float grad, const TeacherSums &ts,
+                                                    const Stats &st) {
+    const float c = kLog2e * p.inv_tau;
+    GradientRow r;
+    r.g = grad * p.inv_tau;
+    r.none = !ts.some || r.g == 0.0f;
+    r.base = base_of(st.m_rest);
+    r.factor = st.inv * exp_scaled(r.base, base_of(st.m), c);
+    if (st.m_rest == -INFINITY) r.factor = st.inv != st.inv ? st.inv : 0.0f;
+    r.factor = r.g * (r.factor - ts.rest * st.inv_rest);
+    return r;
+}
+
+// The gradients of the entries in a segment.
+template <class T>
+__device__ __forceinline__ void write_entries(const DistillParams &p, T *dz, uint32_t lo, uint32_t n, const Stats &st,
+                                              const GradientRow &r, const Entries &e) {
+    const float c = kLog2e * p.inv_tau, all = base_of(st.m);
+    for (uint32_t i = threadIdx.x; i < p.k; i += blockDim.x) {
+        const uint32_t at = (uint32_t)e.at[i] - lo;
+        if (e.at[i] >= 0 && at < n) dz[at] = (T)(r.g * (exp_scaled(e.z[i], all, c) * st.inv - e.p[i]));
+    }
 }
 
 // The gradient of a segment.
@@ -243,9 +309,9 @@ __device__ __forceinline__ void write_gradient(const DistillParams &p, uint32_t 
     const float c = kLog2e * p.inv_tau;
     const T *z = (const T *)p.z + (uint64_t)row * p.ldz + lo;
     T *dz = (T *)p.dz + (uint64_t)row * p.lddz + lo;
-    const float g = p.grad ? p.grad[row] * p.inv_tau : p.inv_tau;
+    const GradientRow r = gradient_row(p, p.grad ? p.grad[row] : 1.0f, ts, st);
     const uint32_t step = blockDim.x * 8;
-    if (!ts.some || g == 0.0f) {
+    if (r.none) {
         const float none[8] = {};
         for (uint32_t i = threadIdx.x * 8; i < n; i += step) {
             if (i + 8 <= n) store8(dz + i, none);
@@ -254,25 +320,18 @@ __device__ __forceinline__ void write_gradient(const DistillParams &p, uint32_t 
         }
         return;
     }
-    const float base = base_of(st.m_rest), all = base_of(st.m);
-    float factor = st.inv * exp_scaled(base, all, c);
-    if (st.m_rest == -INFINITY) factor = st.inv != st.inv ? st.inv : 0.0f;
-    factor = g * (factor - ts.rest * st.inv_rest);
     for (uint32_t i = threadIdx.x * 8; i < n; i += step) {
         float x[8];
         load_upto8(z + i, (int64_t)n - i, -INFINITY, x);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = factor * exp_scaled(x[j], base, c);
+        for (int j = 0; j < 8; ++j) x[j] = r.factor * exp_scaled(x[j], r.base, c);
         if (i + 8 <= n) store8(dz + i, x);
         else
             for (uint32_t j = i; j < n; ++j) dz[j] = (T)x[j - i];
     }
     // The entries' gradients replace what the loop left there, once it is written.
     __syncthreads();
-    for (uint32_t i = threadIdx.x; i < p.k; i += blockDim.x) {
-        const uint32_t at = (uint32_t)e.at[i] - lo;
-        if (e.at[i] >= 0 && at < n) dz[at] = (T)(g * (exp_scaled(e.z[i], all, c) * st.inv - e.p[i]));
-    }
+    write_entries(p, dz, lo, n, st, r, e);
 }
 
 // One workgroup a row: loss and statistics, and with GRAD the gradient.
@@ -284,13 +343,177 @@ __global__ __launch_bounds__(kDT) void distill_row_kernel(DistillParams p) {
     if (block >= p.rows) return;
     const uint32_t row = (uint32_t)block;
     const float c = kLog2e * p.inv_tau;
-    const TeacherSums ts = read_entries<T>(p, row, e);
+    const TeacherSums ts = read_entries<T>(p, row, e, first_entry(p, row));
     if (p.teacher_lse) mark_entries(e, p.k, 0, p.vocab, bits);
     const T *z = (const T *)p.z + (uint64_t)row * p.ldz;
     const Pair v = block_join(scan_segment(z, p.vocab, p.teacher_lse ? bits : nullptr, c), c, e.red);
     const Stats st = finish_row(p, row, ts, v, e);
     if (p.stats && threadIdx.x == 0) ((float4 *)p.stats)[row] = make_float4(st.m, st.inv, st.m_rest, st.inv_rest);
     if (GRAD) write_gradient<T>(p, row, 0, p.vocab, ts, st, e);
+}
+
+// The logits in a chunk's words.
+__device__ __forceinline__ void unpack(const uint32_t (&w)[8], float (&f)[8], float) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(w[j]);
+}
+__device__ __forceinline__ void unpack(const uint32_t (&w)[4], float (&f)[8], bf16) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        f[2 * j] = __uint_as_float(w[j] << 16);
+        f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ void unpack(const uint32_t (&w)[4], float (&f)[8], f16) {
+    typedef f16 pair __attribute__((ext_vector_type(2)));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const pair v = __builtin_bit_cast(pair, w[j]);
+        f[2 * j] = (float)v[0];
+        f[2 * j + 1] = (float)v[1];
+    }
+}
+// Makes the compiler take a value as new, so that what it derived from it before
+// (here: the row in fp32) is not kept in registers for its next use.
+__device__ __forceinline__ void keep(uint32_t &v) { asm volatile("" : "+v"(v)); }
+
+// The same with the row held in registers: THREADS threads of NC chunks of eight
+// logits, and one entry a thread (k is at most THREADS). All loads are issued at
+// once, the entries' before the row's and the student's logits at the entries
+// behind them: loads return in order, so the teacher's sums are made while the row
+// is on its way. A thread takes its chunks into its pair as they land, and the
+// gradient is made from the registers, so a row is read once. Where the row does
+// not fill its last chunk, that starts earlier and overlaps the one before.
+template <class T, int THREADS, int NC, bool GRAD>
+__global__ __launch_bounds__(THREADS) void distill_resident_kernel(DistillParams p) {
+    __shared__ uint32_t bits[THREADS * NC / 4];
+    __shared__ float red[4][16];
+    constexpr int kWords = 2 * sizeof(T);  // of a chunk
+    constexpr uint32_t kWaves = THREADS / 64;
+    const uint64_t block = block_index();
+    if (block >= p.rows) return;
+    const uint32_t row = (uint32_t)block;
+    const float c = kLog2e * p.inv_tau;
+    const bool tail = p.teacher_lse != nullptr;
+    const T *z = (const T *)p.z + (uint64_t)row * p.ldz;
+    uint32_t tid = threadIdx.x;
+    const uint32_t lane = tid & 63, wave = tid >> 6;
+    const auto start = [&](int i) { return min((i * THREADS + tid) * 8, p.vocab - 8); };
+    const auto past = [&](int i) { return (i * THREADS + tid) * 8 - start(i); };  // logits of the chunk before
+
+    const float grad = GRAD && p.grad ? p.grad[row] : 1.0f, lse = tail ? p.teacher_lse[row] : 0.0f;
+    const RawEntry raw = load_entry(p, row, min(tid, max(p.k, 1u) - 1));
+    uint32_t x[NC][kWords];
+#pragma unroll
+    for (int i = 0; i < NC; ++i) __builtin_memcpy(x[i], z + start(i), sizeof(x[i]));
+    if (tail)
+        for (uint32_t i = tid; i < (p.vocab + 31) / 32; i += THREADS) bits[i] = 0;
+    const int at = tid < p.k ? entry_index(p, raw) : -1;
+    const T zt_raw = z[max(at, 0)];
+    const float t = at >= 0 ? entry_logit(p, raw) * p.inv_tau : -INFINITY;
+
+    // The teacher: with a remainder p follows from lse, else from the entries' pair.
+    Pair te = {t, at >= 0 && t != -INFINITY ? 1.0f : 0.0f};
+    float prob = tail && at >= 0 ? expf(t - lse) : 0.0f;
+    if (tail) te = {0.0f, wave_sum(prob)};
+    else te = wave_join(te, kLog2e);
+    const bool any = __ballot(at >= 0) != 0;
+    if (lane == 0) {
+        red[0][wave] = te.m;
+        red[1][wave] = te.s;
+        red[2][wave] = any ? 1.0f : 0.0f;
+    }
+    __syncthreads();
+    const bool in = lane < kWaves;
+    TeacherSums ts;
+    ts.some = __ballot(in && red[2][in ? lane : 0] != 0.0f) != 0;
+    if (tail) {
+        const float sum = wave_sum(in ? red[1][lane] : 0.0f);
+        ts.shift = lse;
+        ts.rest = sum >= 1.0f ? 0.0f : 1.0f - sum;  // NaN stays
+        if (at >= 0) atomicOr(&bits[at / 32], 1u << (at % 32));
+    } else {
+        te = wave_join({in ? red[0][lane] : -INFINITY, in ? red[1][lane] : 0.0f}, kLog2e);
+        ts.shift = base_of(te.m) + logf(te.s);
+        ts.rest = 0.0f;
+        prob = at >= 0 ? exp_scaled(t, base_of(te.m), kLog2e) * inverse(te.s) : 0.0f;
+    }
+    __syncthreads();
+
+    Pair v = {-INFINITY, 0.0f};
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+        float f[8];
+        keep(tid);
+        unpack(x[i], f, T{});
+        const uint32_t skip = past(i);
+        uint32_t out = 0;  // logits that are not taken
+        if (tail) out = bits[start(i) / 32] >> (start(i) % 32) & 255u;
+        if (skip) {  // an overlapping chunk, or one past the row
+            if (tail)
+                for (int j = 0; j < 8; ++j) out |= (bits[(start(i) + j) / 32] >> ((start(i) + j) % 32) & 1u) << j;
+            out |= skip >= 8 ? 255u : (1u << skip) - 1u;
+        }
+        if (out) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = out >> j & 1 ? -INFINITY : f[j];
+        }
+        take8(v, f, c);
+        asm volatile("" : "+v"(v.s));  // now: put off, it would keep the chunk's eight values in registers
+    }
+
+    const float zt = at >= 0 ? (float)zt_raw : -INFINITY;
+    v = wave_join(v, c);
+    Pair top = {zt, at >= 0 ? 1.0f : 0.0f};
+    if (tail) top = wave_join(top, c);
+    if (lane == 0) {
+        red[0][wave] = v.m;
+        red[1][wave] = v.s;
+        red[2][wave] = top.m;
+        red[3][wave] = top.s;
+    }
+    __syncthreads();
+    v = wave_join({in ? red[0][lane] : -INFINITY, in ? red[1][lane] : 0.0f}, c);
+    Pair all = v;
+    if (tail) all = join(v, wave_join({in ? red[2][lane] : -INFINITY, in ? red[3][lane] : 0.0f}, c), c);
+    const Stats st = {all.m, inverse(all.s), v.m, inverse(v.s)};
+    if (p.stats && tid == 0) ((float4 *)p.stats)[row] = make_float4(st.m, st.inv, st.m_rest, st.inv_rest);
+
+    // loss
+    const float log_sum = logf(all.s), base = base_of(all.m);
+    float loss = 0.0f;
+    if (at >= 0 && prob != 0.0f)
+        loss = prob * (t - ts.shift - (all.s == 0.0f ? -INFINITY : (zt - base) * p.inv_tau - log_sum));
+    loss = wave_sum(loss);
+    __syncthreads();
+    if (lane == 0) red[0][wave] = loss;
+    __syncthreads();
+    if (wave == 0) {
+        loss = wave_sum(in ? red[0][lane] : 0.0f) + rest_loss(p, ts, v, base, log_sum);
+        if (lane == 0) p.loss[row] = ts.some ? loss : 0.0f;
+    }
+    if (!GRAD) return;
+
+    T *dz = (T *)p.dz + (uint64_t)row * p.lddz;
+    const GradientRow g = gradient_row(p, grad, ts, st);
+    if (g.none) {
+        const float none[8] = {};
+        for (uint32_t i = tid * 8; i < p.vocab; i += THREADS * 8) store8(dz + min(i, p.vocab - 8), none);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+        float f[8];
+        keep(tid);
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) keep(x[i][w]);
+        unpack(x[i], f, T{});
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = g.factor * exp_scaled(f[j], g.base, c);
+        if (past(i) < 8) store8(dz + start(i), f);
+    }
+    __syncthreads();
+    if (at >= 0) dz[at] = (T)(g.g * (exp_scaled(zt, base, c) * st.inv - prob));
 }
 
 // A row's segment: its pair.
@@ -305,8 +528,7 @@ __global__ __launch_bounds__(kDT) void distill_part_kernel(DistillParams p) {
     const float c = kLog2e * p.inv_tau;
     if (p.teacher_lse) {
         for (uint32_t i = threadIdx.x; i < p.k; i += blockDim.x) {
-            const int64_t at = read_index(p.idx, p.itype, (uint64_t)row * p.ldi + i);
-            e.at[i] = at >= 0 && at < (int64_t)p.vocab ? (int)at : -1;
+            e.at[i] = entry_index(p, load_entry(p, row, i));
         }
         mark_entries(e, p.k, lo, n, bits);  // a thread reads back its own entries
     }
@@ -323,7 +545,7 @@ __global__ __launch_bounds__(256) void distill_join_kernel(DistillParams p) {
     if (block >= p.rows) return;
     const uint32_t row = (uint32_t)block;
     const float c = kLog2e * p.inv_tau;
-    const TeacherSums ts = read_entries<T>(p, row, e);
+    const TeacherSums ts = read_entries<T>(p, row, e, first_entry(p, row));
     Pair v = {-INFINITY, 0.0f};
     for (uint32_t i = threadIdx.x; i < p.segments; i += blockDim.x) {
         const float2 q = p.part[(uint64_t)row * p.segments + i];
@@ -342,7 +564,7 @@ __global__ __launch_bounds__(kDT) void distill_gradient_kernel(DistillParams p) 
     if (block >= (uint64_t)p.rows * p.segments) return;
     const uint32_t row = (uint32_t)(block / p.segments), seg = (uint32_t)(block % p.segments);
     const uint32_t lo = seg * p.segment, n = min(p.segment, p.vocab - lo);
-    const TeacherSums ts = read_entries<T>(p, row, e);
+    const TeacherSums ts = read_entries<T>(p, row, e, first_entry(p, row));
     const float4 s = ((const float4 *)p.stats_in)[row];
     write_gradient<T>(p, row, lo, n, ts, Stats{s.x, s.y, s.z, s.w}, e);
 }

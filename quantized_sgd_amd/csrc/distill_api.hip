@@ -56,6 +56,27 @@ DistillParams params_of(const void *z, uint64_t rows, uint64_t vocab, uint64_t l
 // Workspace of a split: the segments' pairs, then a row's statistics.
 uint64_t pair_bytes(const DistillParams &p) { return round_up((uint64_t)p.rows * p.segments * 8, 256); }
 
+template <class T, int THREADS, int NC, bool GRAD>
+void launch_resident(const DistillParams &p, hipStream_t stream) {
+    distill_resident_kernel<T, THREADS, NC, GRAD><<<grid_of(p.rows), THREADS, 0, stream>>>(p);
+}
+
+// One workgroup a row, with the row in registers where it fits: 64 VGPRs of it for
+// each of 1024 threads at most (131072 logits of 16 bits, 65536 of 32). A thread
+// takes one entry, so rows of many entries take more threads.
+template <class T, bool GRAD>
+void launch_rows(const DistillParams &p, hipStream_t stream) {
+    const uint64_t chunks = div_up(p.vocab, 8);
+    const uint32_t k = p.k;
+    if (p.vocab < 8 || chunks > (sizeof(T) == 2 ? 16 : 8) * 1024) distill_row_kernel<T, GRAD><<<grid_of(p.rows), kDT, 0, stream>>>(p);
+    else if (chunks <= 256 && k <= 256) launch_resident<T, 256, 1, GRAD>(p, stream);
+    else if (chunks <= 1024 && k <= 256) launch_resident<T, 256, 4, GRAD>(p, stream);
+    else if (chunks <= 2048 && k <= 512) launch_resident<T, 512, 4, GRAD>(p, stream);
+    else if (chunks <= 4096) launch_resident<T, 1024, 4, GRAD>(p, stream);
+    else if (chunks <= 8192) launch_resident<T, 1024, 8, GRAD>(p, stream);
+    else if constexpr (sizeof(T) == 2) launch_resident<T, 1024, 16, GRAD>(p, stream);
+}
+
 template <class T>
 void launch_stats(DistillParams p, void *workspace, hipStream_t stream) {
     p.part = (float2 *)workspace;
@@ -87,7 +108,7 @@ qsgd_status qsgd_distill_forward(const void *z, qsgd_dtype dtype, uint64_t rows,
     p.stats = stats;
     return with_type(dtype, [&](auto t) {
         using T = decltype(t);
-        if (p.segments == 1) distill_row_kernel<T, false><<<grid_of(rows), kDT, 0, stream>>>(p);
+        if (p.segments == 1) launch_rows<T, false>(p, stream);
         else launch_stats<T>(p, workspace, stream);
         return launched();
     });
@@ -125,7 +146,7 @@ qsgd_status qsgd_distill_step(const void *z, qsgd_dtype dtype, uint64_t rows, ui
     return with_type(dtype, [&](auto t) {
         using T = decltype(t);
         if (p.segments == 1) {
-            distill_row_kernel<T, true><<<grid_of(rows), kDT, 0, stream>>>(p);
+            launch_rows<T, true>(p, stream);
         } else {
             p.stats = (float *)((char *)workspace + pair_bytes(p));
             p.stats_in = p.stats;

@@ -40,28 +40,45 @@ __device__ __forceinline__ void load_upto8(const T *p, int64_t left, float fill,
     else load_part(p, (int)left, fill, f);
 }
 
+// Two at a time: gfx950 rounds a pair to bfloat16 in one instruction.
 template <class T>
 __device__ __forceinline__ void store8(T *p, const float (&f)[8]) {
-    T v[8];
+    typedef float pair32 __attribute__((ext_vector_type(2)));
+    typedef T pair __attribute__((ext_vector_type(2)));
+    pair v[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = (T)f[i];
+    for (int i = 0; i < 4; ++i) v[i] = __builtin_convertvector((pair32){f[2 * i], f[2 * i + 1]}, pair);
     __builtin_memcpy(p, v, sizeof(v));
 }
 
+// Reductions over a wave in registers: rows of 16 lanes by shifts, then the rows'
+// last lanes broadcast on. Lane 63 has the result, which all lanes get.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp(uint32_t none, uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp((int)none, (int)v, CTRL, ROWS, 0xf, false);
+}
+template <class F>
+__device__ __forceinline__ uint32_t wave_reduce(uint32_t v, uint32_t none, F f) {
+    v = f(v, dpp<0x111, 0xf>(none, v));  // row_shr 1, 2, 4, 8
+    v = f(v, dpp<0x112, 0xf>(none, v));
+    v = f(v, dpp<0x114, 0xf>(none, v));
+    v = f(v, dpp<0x118, 0xf>(none, v));
+    v = f(v, dpp<0x142, 0xa>(none, v));  // row_bcast 15, 31
+    v = f(v, dpp<0x143, 0xc>(none, v));
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
 __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-#pragma unroll
-    for (int o = 32; o; o >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, o));
-    return v;
+    return wave_reduce(v, 0u, [](uint32_t a, uint32_t b) { return max(a, b); });
 }
 __device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-    for (int o = 32; o; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
-    return v;
+    return __uint_as_float(wave_reduce(__float_as_uint(v), 0xff800000u, [](uint32_t a, uint32_t b) {
+        return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+    }));
 }
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
-    return v;
+    return __uint_as_float(wave_reduce(__float_as_uint(v), 0u, [](uint32_t a, uint32_t b) {
+        return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+    }));
 }
 
 // A launch of `blocks` workgroups as a grid of two dimensions (one dimension of a
