@@ -384,7 +384,9 @@ __device__ __forceinline__ void keep(uint32_t &v) { asm volatile("" : "+v"(v)); 
 // is on its way. A thread takes its chunks into its pair as they land, and the
 // gradient is made from the registers, so a row is read once. Where the row does
 // not fill its last chunk, that starts earlier and overlaps the one before.
-template <class T, int THREADS, int NC, bool GRAD>
+enum { kLoss, kStep, kGradient };  // what a call of it makes; kGradient takes the statistics from memory
+
+template <class T, int THREADS, int NC, int MAKE>
 __global__ __launch_bounds__(THREADS) void distill_resident_kernel(DistillParams p) {
     __shared__ uint32_t bits[THREADS * NC / 4];
     __shared__ float red[4][16];
@@ -395,18 +397,19 @@ __global__ __launch_bounds__(THREADS) void distill_resident_kernel(DistillParams
     const uint32_t row = (uint32_t)block;
     const float c = kLog2e * p.inv_tau;
     const bool tail = p.teacher_lse != nullptr;
+    const bool marks = tail && MAKE != kGradient;
     const T *z = (const T *)p.z + (uint64_t)row * p.ldz;
     uint32_t tid = threadIdx.x;
     const uint32_t lane = tid & 63, wave = tid >> 6;
     const auto start = [&](int i) { return min((i * THREADS + tid) * 8, p.vocab - 8); };
     const auto past = [&](int i) { return (i * THREADS + tid) * 8 - start(i); };  // logits of the chunk before
 
-    const float grad = GRAD && p.grad ? p.grad[row] : 1.0f, lse = tail ? p.teacher_lse[row] : 0.0f;
+    const float grad = MAKE != kLoss && p.grad ? p.grad[row] : 1.0f, lse = tail ? p.teacher_lse[row] : 0.0f;
     const RawEntry raw = load_entry(p, row, min(tid, max(p.k, 1u) - 1));
     uint32_t x[NC][kWords];
 #pragma unroll
     for (int i = 0; i < NC; ++i) __builtin_memcpy(x[i], z + start(i), sizeof(x[i]));
-    if (tail)
+    if (marks)
         for (uint32_t i = tid; i < (p.vocab + 31) / 32; i += THREADS) bits[i] = 0;
     const int at = tid < p.k ? entry_index(p, raw) : -1;
     const T zt_raw = z[max(at, 0)];
@@ -431,7 +434,7 @@ __global__ __launch_bounds__(THREADS) void distill_resident_kernel(DistillParams
         const float sum = wave_sum(in ? red[1][lane] : 0.0f);
         ts.shift = lse;
         ts.rest = sum >= 1.0f ? 0.0f : 1.0f - sum;  // NaN stays
-        if (at >= 0) atomicOr(&bits[at / 32], 1u << (at % 32));
+        if (marks && at >= 0) atomicOr(&bits[at / 32], 1u << (at % 32));
     } else {
         te = wave_join({in ? red[0][lane] : -INFINITY, in ? red[1][lane] : 0.0f}, kLog2e);
         ts.shift = base_of(te.m) + logf(te.s);
@@ -440,60 +443,66 @@ __global__ __launch_bounds__(THREADS) void distill_resident_kernel(DistillParams
     }
     __syncthreads();
 
-    Pair v = {-INFINITY, 0.0f};
+    Stats st;
+    if constexpr (MAKE == kGradient) {
+        const float4 s = ((const float4 *)p.stats_in)[row];
+        st = {s.x, s.y, s.z, s.w};
+    } else {
+        Pair v = {-INFINITY, 0.0f};
 #pragma unroll
-    for (int i = 0; i < NC; ++i) {
-        float f[8];
-        keep(tid);
-        unpack(x[i], f, T{});
-        const uint32_t skip = past(i);
-        uint32_t out = 0;  // logits that are not taken
-        if (tail) out = bits[start(i) / 32] >> (start(i) % 32) & 255u;
-        if (skip) {  // an overlapping chunk, or one past the row
-            if (tail)
-                for (int j = 0; j < 8; ++j) out |= (bits[(start(i) + j) / 32] >> ((start(i) + j) % 32) & 1u) << j;
-            out |= skip >= 8 ? 255u : (1u << skip) - 1u;
-        }
-        if (out) {
+        for (int i = 0; i < NC; ++i) {
+            float f[8];
+            keep(tid);
+            unpack(x[i], f, T{});
+            const uint32_t skip = past(i);
+            uint32_t out = 0;  // logits that are not taken
+            if (tail) out = bits[start(i) / 32] >> (start(i) % 32) & 255u;
+            if (skip) {  // an overlapping chunk, or one past the row
+                if (tail)
+                    for (int j = 0; j < 8; ++j) out |= (bits[(start(i) + j) / 32] >> ((start(i) + j) % 32) & 1u) << j;
+                out |= skip >= 8 ? 255u : (1u << skip) - 1u;
+            }
+            if (out) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = out >> j & 1 ? -INFINITY : f[j];
+                for (int j = 0; j < 8; ++j) f[j] = out >> j & 1 ? -INFINITY : f[j];
+            }
+            take8(v, f, c);
+            asm volatile("" : "+v"(v.s));  // now: put off, it would keep the chunk's eight values in registers
         }
-        take8(v, f, c);
-        asm volatile("" : "+v"(v.s));  // now: put off, it would keep the chunk's eight values in registers
+
+        v = wave_join(v, c);
+        Pair top = {at >= 0 ? (float)zt_raw : -INFINITY, at >= 0 ? 1.0f : 0.0f};
+        if (tail) top = wave_join(top, c);
+        if (lane == 0) {
+            red[0][wave] = v.m;
+            red[1][wave] = v.s;
+            red[2][wave] = top.m;
+            red[3][wave] = top.s;
+        }
+        __syncthreads();
+        v = wave_join({in ? red[0][lane] : -INFINITY, in ? red[1][lane] : 0.0f}, c);
+        Pair all = v;
+        if (tail) all = join(v, wave_join({in ? red[2][lane] : -INFINITY, in ? red[3][lane] : 0.0f}, c), c);
+        st = {all.m, inverse(all.s), v.m, inverse(v.s)};
+        if (p.stats && tid == 0) ((float4 *)p.stats)[row] = make_float4(st.m, st.inv, st.m_rest, st.inv_rest);
+
+        // loss
+        const float log_sum = logf(all.s), base = base_of(all.m), zt = at >= 0 ? (float)zt_raw : -INFINITY;
+        float loss = 0.0f;
+        if (at >= 0 && prob != 0.0f)
+            loss = prob * (t - ts.shift - (all.s == 0.0f ? -INFINITY : (zt - base) * p.inv_tau - log_sum));
+        loss = wave_sum(loss);
+        __syncthreads();
+        if (lane == 0) red[0][wave] = loss;
+        __syncthreads();
+        if (wave == 0) {
+            loss = wave_sum(in ? red[0][lane] : 0.0f) + rest_loss(p, ts, v, base, log_sum);
+            if (lane == 0) p.loss[row] = ts.some ? loss : 0.0f;
+        }
     }
+    if (MAKE == kLoss) return;
 
     const float zt = at >= 0 ? (float)zt_raw : -INFINITY;
-    v = wave_join(v, c);
-    Pair top = {zt, at >= 0 ? 1.0f : 0.0f};
-    if (tail) top = wave_join(top, c);
-    if (lane == 0) {
-        red[0][wave] = v.m;
-        red[1][wave] = v.s;
-        red[2][wave] = top.m;
-        red[3][wave] = top.s;
-    }
-    __syncthreads();
-    v = wave_join({in ? red[0][lane] : -INFINITY, in ? red[1][lane] : 0.0f}, c);
-    Pair all = v;
-    if (tail) all = join(v, wave_join({in ? red[2][lane] : -INFINITY, in ? red[3][lane] : 0.0f}, c), c);
-    const Stats st = {all.m, inverse(all.s), v.m, inverse(v.s)};
-    if (p.stats && tid == 0) ((float4 *)p.stats)[row] = make_float4(st.m, st.inv, st.m_rest, st.inv_rest);
-
-    // loss
-    const float log_sum = logf(all.s), base = base_of(all.m);
-    float loss = 0.0f;
-    if (at >= 0 && prob != 0.0f)
-        loss = prob * (t - ts.shift - (all.s == 0.0f ? -INFINITY : (zt - base) * p.inv_tau - log_sum));
-    loss = wave_sum(loss);
-    __syncthreads();
-    if (lane == 0) red[0][wave] = loss;
-    __syncthreads();
-    if (wave == 0) {
-        loss = wave_sum(in ? red[0][lane] : 0.0f) + rest_loss(p, ts, v, base, log_sum);
-        if (lane == 0) p.loss[row] = ts.some ? loss : 0.0f;
-    }
-    if (!GRAD) return;
-
     T *dz = (T *)p.dz + (uint64_t)row * p.lddz;
     const GradientRow g = gradient_row(p, grad, ts, st);
     if (g.none) {
@@ -510,10 +519,16 @@ __global__ __launch_bounds__(THREADS) void distill_resident_kernel(DistillParams
         unpack(x[i], f, T{});
 #pragma unroll
         for (int j = 0; j < 8; ++j) f[j] = g.factor * exp_scaled(f[j], g.base, c);
-        if (past(i) < 8) store8(dz + start(i), f);
+        const uint32_t skip = past(i);
+        if (skip == 0) {
+            store8(dz + start(i), f);
+        } else if (skip < 8) {  // the chunk before writes the rest: in place, this one may have read it from there
+            for (int j = 0; j < 8; ++j)
+                if (j >= (int)skip) dz[start(i) + j] = (T)f[j];
+        }
     }
     __syncthreads();
-    if (at >= 0) dz[at] = (T)(g.g * (exp_scaled(zt, base, c) * st.inv - prob));
+    if (at >= 0) dz[at] = (T)(g.g * (exp_scaled(zt, base_of(st.m), c) * st.inv - prob));
 }
 
 // A row's segment: its pair.

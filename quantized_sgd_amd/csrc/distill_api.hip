@@ -56,25 +56,32 @@ DistillParams params_of(const void *z, uint64_t rows, uint64_t vocab, uint64_t l
 // Workspace of a split: the segments' pairs, then a row's statistics.
 uint64_t pair_bytes(const DistillParams &p) { return round_up((uint64_t)p.rows * p.segments * 8, 256); }
 
-template <class T, int THREADS, int NC, bool GRAD>
-void launch_resident(const DistillParams &p, hipStream_t stream) {
-    distill_resident_kernel<T, THREADS, NC, GRAD><<<grid_of(p.rows), THREADS, 0, stream>>>(p);
+// Rows with one workgroup each are held in registers where they fit: 80 VGPRs of a
+// row for each of 1024 threads at most (163840 logits of 16 bits), 64 for logits of
+// 32 bits (65536).
+template <class T>
+bool resident(uint64_t vocab) {
+    return vocab >= 8 && vocab <= (sizeof(T) == 2 ? 163840 : 65536);
 }
 
-// One workgroup a row, with the row in registers where it fits: 64 VGPRs of it for
-// each of 1024 threads at most (131072 logits of 16 bits, 65536 of 32). A thread
-// takes one entry, so rows of many entries take more threads.
-template <class T, bool GRAD>
-void launch_rows(const DistillParams &p, hipStream_t stream) {
-    const uint64_t chunks = div_up(p.vocab, 8);
-    const uint32_t k = p.k;
-    if (p.vocab < 8 || chunks > (sizeof(T) == 2 ? 16 : 8) * 1024) distill_row_kernel<T, GRAD><<<grid_of(p.rows), kDT, 0, stream>>>(p);
-    else if (chunks <= 256 && k <= 256) launch_resident<T, 256, 1, GRAD>(p, stream);
-    else if (chunks <= 1024 && k <= 256) launch_resident<T, 256, 4, GRAD>(p, stream);
-    else if (chunks <= 2048 && k <= 512) launch_resident<T, 512, 4, GRAD>(p, stream);
-    else if (chunks <= 4096) launch_resident<T, 1024, 4, GRAD>(p, stream);
-    else if (chunks <= 8192) launch_resident<T, 1024, 8, GRAD>(p, stream);
-    else if constexpr (sizeof(T) == 2) launch_resident<T, 1024, 16, GRAD>(p, stream);
+template <class T, int THREADS, int NC, int MAKE>
+void launch_chunks(const DistillParams &p, hipStream_t stream) {
+    distill_resident_kernel<T, THREADS, NC, MAKE><<<grid_of(p.rows), THREADS, 0, stream>>>(p);
+}
+
+// A thread takes one entry, so rows of many entries take more threads.
+template <class T, int MAKE>
+void launch_resident(const DistillParams &p, hipStream_t stream) {
+    const uint32_t chunks = (uint32_t)div_up(p.vocab, 8), k = p.k;
+    if (chunks <= 256 && k <= 256) launch_chunks<T, 256, 1, MAKE>(p, stream);
+    else if (chunks <= 1024 && k <= 256) launch_chunks<T, 256, 4, MAKE>(p, stream);
+    else if (chunks <= 2048 && k <= 512) launch_chunks<T, 512, 4, MAKE>(p, stream);
+    else if (chunks <= 4096) launch_chunks<T, 1024, 4, MAKE>(p, stream);
+    else if (chunks <= 8192) launch_chunks<T, 1024, 8, MAKE>(p, stream);
+    else if constexpr (sizeof(T) == 2) {
+        if (chunks <= 16384) launch_chunks<T, 1024, 16, MAKE>(p, stream);
+        else launch_chunks<T, 1024, 20, MAKE>(p, stream);
+    }
 }
 
 template <class T>
@@ -108,8 +115,9 @@ qsgd_status qsgd_distill_forward(const void *z, qsgd_dtype dtype, uint64_t rows,
     p.stats = stats;
     return with_type(dtype, [&](auto t) {
         using T = decltype(t);
-        if (p.segments == 1) launch_rows<T, false>(p, stream);
-        else launch_stats<T>(p, workspace, stream);
+        if (p.segments > 1) launch_stats<T>(p, workspace, stream);
+        else if (resident<T>(vocab)) launch_resident<T, kLoss>(p, stream);
+        else distill_row_kernel<T, false><<<grid_of(rows), kDT, 0, stream>>>(p);
         return launched();
     });
 }
@@ -126,7 +134,9 @@ qsgd_status qsgd_distill_backward(const void *z, qsgd_dtype dtype, uint64_t rows
     p.dz = dz;
     p.lddz = lddz;
     return with_type(dtype, [&](auto t) {
-        distill_gradient_kernel<decltype(t)><<<grid_of(rows * p.segments), kDT, 0, stream>>>(p);
+        using T = decltype(t);
+        if (p.segments == 1 && resident<T>(vocab)) launch_resident<T, kGradient>(p, stream);
+        else distill_gradient_kernel<T><<<grid_of(rows * p.segments), kDT, 0, stream>>>(p);
         return launched();
     });
 }
@@ -145,8 +155,10 @@ qsgd_status qsgd_distill_step(const void *z, qsgd_dtype dtype, uint64_t rows, ui
     p.lddz = lddz;
     return with_type(dtype, [&](auto t) {
         using T = decltype(t);
-        if (p.segments == 1) {
-            launch_rows<T, true>(p, stream);
+        if (p.segments == 1 && resident<T>(vocab)) {
+            launch_resident<T, kStep>(p, stream);
+        } else if (p.segments == 1) {
+            distill_row_kernel<T, true><<<grid_of(rows), kDT, 0, stream>>>(p);
         } else {
             p.stats = (float *)((char *)workspace + pair_bytes(p));
             p.stats_in = p.stats;
