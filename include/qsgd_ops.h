@@ -148,10 +148,10 @@ qsgd_status qsgd_int8_linear_backward(const void *gy, qsgd_dtype dtype, uint64_t
  *          backward call takes, with the same z, idx, t, tau and teacher_lse.
  *   dz     [rows, vocab] output of z's type, row stride lddz; may be z itself
  *          (same pointer and stride), not otherwise overlap it.
- *   workspace  qsgd_distill_workspace(rows, vocab) bytes.
+ *   workspace  qsgd_distill_workspace(rows, vocab, dtype) bytes.
  */
 uint32_t qsgd_distill_max_entries(void);
-uint64_t qsgd_distill_workspace(uint64_t rows, uint64_t vocab);
+uint64_t qsgd_distill_workspace(uint64_t rows, uint64_t vocab, qsgd_dtype dtype);
 
 /* The entries of a call and how they are read. */
 typedef struct {

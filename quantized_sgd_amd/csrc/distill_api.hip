@@ -10,13 +10,20 @@ using namespace qsgd::ops;
 
 namespace {
 
+// Rows held in registers by one workgroup: 80 VGPRs of a row for each of 1024 threads
+// at most (163840 logits of 16 bits), 64 for logits of 32 bits (65536).
+bool resident(uint64_t vocab, qsgd_dtype dtype) {
+    return vocab >= 8 && vocab <= (bytes_of(dtype) == 2 ? 163840 : 65536);
+}
+
 struct Split {
     uint32_t segments, segment;
 };
 
-// One workgroup a row where there are rows enough for the chip; else segments of
-// at least 8192 logits. The gradient's segments may differ from the loss's.
-Split split_rows(uint64_t rows, uint64_t vocab) {
+// One workgroup a row where that holds it in registers or there are rows enough for
+// the chip; else segments of at least 8192 logits.
+Split split_rows(uint64_t rows, uint64_t vocab, qsgd_dtype dtype) {
+    if (resident(vocab, dtype)) return {1, (uint32_t)vocab};
     uint64_t segments = std::max<uint64_t>(1, div_up(vocab, kMaxSegment));
     if (rows < 256) segments = std::max(segments, std::min(div_up(512, std::max<uint64_t>(rows, 1)), vocab / 8192));
     const uint64_t segment = round_up(std::max<uint64_t>(1, div_up(vocab, segments)), 8);
@@ -32,7 +39,7 @@ bool args_ok(const void *z, qsgd_dtype dtype, uint64_t rows, uint64_t vocab, uin
     return (!vocab || z) && (!te->k || (te->idx && te->t));
 }
 
-DistillParams params_of(const void *z, uint64_t rows, uint64_t vocab, uint64_t ldz, const qsgd_teacher *te) {
+DistillParams params_of(const void *z, qsgd_dtype dtype, uint64_t rows, uint64_t vocab, uint64_t ldz, const qsgd_teacher *te) {
     DistillParams p{};
     p.z = z;
     p.idx = te->idx;
@@ -47,7 +54,7 @@ DistillParams params_of(const void *z, uint64_t rows, uint64_t vocab, uint64_t l
     p.itype = te->itype;
     p.ttype = te->ttype;
     p.inv_tau = 1.0f / te->tau;
-    const Split s = split_rows(rows, vocab);
+    const Split s = split_rows(rows, vocab, dtype);
     p.segments = s.segments;
     p.segment = s.segment;
     return p;
@@ -55,14 +62,6 @@ DistillParams params_of(const void *z, uint64_t rows, uint64_t vocab, uint64_t l
 
 // Workspace of a split: the segments' pairs, then a row's statistics.
 uint64_t pair_bytes(const DistillParams &p) { return round_up((uint64_t)p.rows * p.segments * 8, 256); }
-
-// Rows with one workgroup each are held in registers where they fit: 80 VGPRs of a
-// row for each of 1024 threads at most (163840 logits of 16 bits), 64 for logits of
-// 32 bits (65536).
-template <class T>
-bool resident(uint64_t vocab) {
-    return vocab >= 8 && vocab <= (sizeof(T) == 2 ? 163840 : 65536);
-}
 
 template <class T, int THREADS, int NC, int MAKE>
 void launch_chunks(const DistillParams &p, hipStream_t stream) {
@@ -97,9 +96,9 @@ extern "C" {
 
 uint32_t qsgd_distill_max_entries(void) { return kMaxEntries; }
 
-uint64_t qsgd_distill_workspace(uint64_t rows, uint64_t vocab) {
-    if (rows > kMaxDim || vocab > kMaxDim || rows == 0) return 0;
-    const Split s = split_rows(rows, vocab);
+uint64_t qsgd_distill_workspace(uint64_t rows, uint64_t vocab, qsgd_dtype dtype) {
+    if (!is_float(dtype) || rows > kMaxDim || vocab > kMaxDim || rows == 0) return 0;
+    const Split s = split_rows(rows, vocab, dtype);
     return s.segments == 1 ? 0 : round_up(rows * s.segments * 8, 256) + rows * 16;
 }
 
@@ -109,14 +108,14 @@ qsgd_status qsgd_distill_forward(const void *z, qsgd_dtype dtype, uint64_t rows,
     if (!args_ok(z, dtype, rows, vocab, ldz, teacher)) return QSGD_ERR_INVALID_ARG;
     if (rows == 0) return QSGD_OK;
     if (!loss || !stats || !aligned_to(stats, 16)) return QSGD_ERR_INVALID_ARG;
-    DistillParams p = params_of(z, rows, vocab, ldz, teacher);
+    DistillParams p = params_of(z, dtype, rows, vocab, ldz, teacher);
     if (p.segments > 1 && (!workspace || !aligned_to(workspace, 16))) return QSGD_ERR_INVALID_ARG;
     p.loss = loss;
     p.stats = stats;
     return with_type(dtype, [&](auto t) {
         using T = decltype(t);
         if (p.segments > 1) launch_stats<T>(p, workspace, stream);
-        else if (resident<T>(vocab)) launch_resident<T, kLoss>(p, stream);
+        else if (resident(vocab, dtype)) launch_resident<T, kLoss>(p, stream);
         else distill_row_kernel<T, false><<<grid_of(rows), kDT, 0, stream>>>(p);
         return launched();
     });
@@ -128,14 +127,14 @@ qsgd_status qsgd_distill_backward(const void *z, qsgd_dtype dtype, uint64_t rows
     if (!args_ok(z, dtype, rows, vocab, ldz, teacher) || lddz < vocab) return QSGD_ERR_INVALID_ARG;
     if (rows == 0 || vocab == 0) return QSGD_OK;
     if (!dz || !stats || !aligned_to(stats, 16)) return QSGD_ERR_INVALID_ARG;
-    DistillParams p = params_of(z, rows, vocab, ldz, teacher);
+    DistillParams p = params_of(z, dtype, rows, vocab, ldz, teacher);
     p.stats_in = stats;
     p.grad = grad;
     p.dz = dz;
     p.lddz = lddz;
     return with_type(dtype, [&](auto t) {
         using T = decltype(t);
-        if (p.segments == 1 && resident<T>(vocab)) launch_resident<T, kGradient>(p, stream);
+        if (resident(vocab, dtype)) launch_resident<T, kGradient>(p, stream);
         else distill_gradient_kernel<T><<<grid_of(rows * p.segments), kDT, 0, stream>>>(p);
         return launched();
     });
@@ -147,7 +146,7 @@ qsgd_status qsgd_distill_step(const void *z, qsgd_dtype dtype, uint64_t rows, ui
     if (!args_ok(z, dtype, rows, vocab, ldz, teacher) || lddz < vocab) return QSGD_ERR_INVALID_ARG;
     if (rows == 0) return QSGD_OK;
     if (!loss || (vocab && !dz)) return QSGD_ERR_INVALID_ARG;
-    DistillParams p = params_of(z, rows, vocab, ldz, teacher);
+    DistillParams p = params_of(z, dtype, rows, vocab, ldz, teacher);
     if (p.segments > 1 && (!workspace || !aligned_to(workspace, 16))) return QSGD_ERR_INVALID_ARG;
     p.loss = loss;
     p.grad = grad;
@@ -155,7 +154,7 @@ qsgd_status qsgd_distill_step(const void *z, qsgd_dtype dtype, uint64_t rows, ui
     p.lddz = lddz;
     return with_type(dtype, [&](auto t) {
         using T = decltype(t);
-        if (p.segments == 1 && resident<T>(vocab)) {
+        if (resident(vocab, dtype)) {
             launch_resident<T, kStep>(p, stream);
         } else if (p.segments == 1) {
             distill_row_kernel<T, true><<<grid_of(rows), kDT, 0, stream>>>(p);

@@ -181,8 +181,8 @@ qsgd_status run_matmul(const Plan &plan, const int8_t *a, const float *sa, const
         using OUT = decltype(t);
         if (plan.skinny) {
             const dim3 grid((uint32_t)div_up(n, 16));
-            if (m <= 16) skinny_kernel<1, 1, OUT><<<grid, 512, 0, stream>>>(p);
-            else skinny_kernel<2, 1, OUT><<<grid, 512, 0, stream>>>(p);
+            if (m <= 16) skinny_kernel<1, int8_t, OUT><<<grid, 512, 0, stream>>>(p);
+            else skinny_kernel<2, int8_t, OUT><<<grid, 512, 0, stream>>>(p);
         } else if (plan.splits == 1) {
             launch_matmul<OUT>(plan, p, stream);
         } else {
@@ -197,6 +197,12 @@ qsgd_status run_matmul(const Plan &plan, const int8_t *a, const float *sa, const
 Plan plan_of(const int8_t *a, uint64_t lda, bool a_padded, const int8_t *b, uint64_t ldb, uint64_t m, uint64_t n,
              uint64_t k) {
     return plan_matmul(aligned_to(a, 16), lda, a_padded, aligned_to(b, 16), ldb, false, m, n, k);
+}
+
+// The layer in one launch: the rows' levels fit 32 KB of LDS (every workgroup makes
+// them for itself) and nobody keeps them.
+bool fuses(uint64_t m, uint64_t n, uint64_t k) {
+    return m <= 16 && n > 0 && n <= (1u << 24) && k <= 32768 && m * fused_pitch((uint32_t)k) <= 32768;
 }
 
 bool dims_ok(uint64_t m, uint64_t n, uint64_t k) { return m <= kMaxDim && n <= kMaxDim && k <= kMaxDim; }
@@ -281,6 +287,7 @@ qsgd_status qsgd_int8_matmul(const int8_t *a, uint64_t lda, const float *sa, con
 
 uint64_t qsgd_int8_linear_workspace(const int8_t *w, uint64_t ldw, uint64_t m, uint64_t n, uint64_t k, int keep) {
     if (!dims_ok(m, n, k) || k > kMaxK || m == 0) return 0;
+    if (!keep && fuses(m, n, k)) return 0;
     const uint64_t ldq = padded16(k);
     uint64_t bytes = n == 0 ? 0 : plan_of(nullptr, ldq, true, w, ldw, m, n, k).bytes;
     if (!keep) bytes += round_up(m * ldq, 256) + round_up(4 * m, 256);
@@ -296,6 +303,14 @@ qsgd_status qsgd_int8_linear(const void *x, qsgd_dtype dtype, uint64_t ldx, cons
     if ((xq == nullptr) != (sx == nullptr)) return QSGD_ERR_INVALID_ARG;
     if (xq && (ldxq < padded16(k) || ldxq % 16 || ldxq > kMaxK || !aligned_to(xq, 16))) return QSGD_ERR_INVALID_ARG;
     if ((k && !x) || (n && (!sw || !y || (k && !w)))) return QSGD_ERR_INVALID_ARG;
+    if (!xq && fuses(m, n, k)) {
+        const MatmulParams p{(const int8_t *)x, w, nullptr, sw, bias, y, nullptr, ldx, ldw, ldy, (uint32_t)m, (uint32_t)n, (uint32_t)k};
+        return with_type(dtype, [&](auto t) {
+            using T = decltype(t);
+            skinny_kernel<1, T, T><<<(uint32_t)div_up(n, 16), 512, m * fused_pitch((uint32_t)k), stream>>>(p);
+            return launched();
+        });
+    }
     const uint64_t need = qsgd_int8_linear_workspace(w, ldw, m, n, k, xq != nullptr);
     if (need && (!workspace || !aligned_to(workspace, 16))) return QSGD_ERR_INVALID_ARG;
     const uint64_t ldq = xq ? ldxq : padded16(k);

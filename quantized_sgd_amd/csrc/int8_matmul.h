@@ -8,6 +8,7 @@
 //  - skinny_kernel: few rows of a (single tokens), bound by reading b once.
 #pragma once
 
+#include "int8_quantize.h"
 #include "ops_common.h"
 
 namespace qsgd {
@@ -399,86 +400,105 @@ __global__ __launch_bounds__(256) void join_kernel(MatmulParams p) {
     }
 }
 
-// Few rows of a: a workgroup of 8 waves takes 16 NT rows of b and all of k, its
-// waves every eighth 64-byte step. b goes from memory to registers in the matrix
-// instruction's own layout (16 bytes of a row a lane), at any alignment; the rows
-// of a, at most 16 MT, come from the caches. The waves' sums meet in LDS.
-template <int MT, int NT, class OUT>
+// Few rows of a: a workgroup of 8 waves takes 16 rows of b and all of k, its waves
+// every eighth 64-byte step. b goes from memory to registers in the matrix
+// instruction's own layout (16 bytes of a row a lane), at any alignment, kAhead
+// steps ahead; the rows of a, at most 16 MT, come from the caches. The waves' sums
+// meet in LDS.
+//
+// X = int8_t: a is quantized. Otherwise a is the layer's input and every workgroup
+// quantizes it into LDS for itself, while its first steps of b are on their way:
+// for the few rows this is made for that costs less than a launch.
+template <int MT, class X, class OUT>
 __global__ __launch_bounds__(512) void skinny_kernel(MatmulParams p) {
-    constexpr int kWaves = 8, kUnroll = 4;
-    __shared__ int32_t sums[kWaves][MT * NT][256];
+    constexpr int kWaves = 8, kAhead = 8;
+    constexpr bool kFused = sizeof(X) > 1;
+    extern __shared__ __align__(16) int8_t xq[];  // kFused: [m, pitch]
+    __shared__ __align__(16) int32_t sums[kWaves][MT][256];
+    __shared__ float sx[kFused ? 16 * MT : 1];
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const uint32_t n0 = blockIdx.x * (16 * NT);
+    const uint32_t n0 = blockIdx.x * 16;
     const uint32_t r = lane & 15, chunk = lane >> 4;
-    const int8_t *b[NT], *a[MT];
-#pragma unroll
-    for (int i = 0; i < NT; ++i) b[i] = p.b + (uint64_t)min(n0 + i * 16 + r, p.n - 1) * p.ldb;
-#pragma unroll
-    for (int j = 0; j < MT; ++j) a[j] = p.a + (uint64_t)min(j * 16 + r, p.m - 1) * p.lda;
-    v4i acc[MT][NT];
-#pragma unroll
-    for (int j = 0; j < MT; ++j)
-#pragma unroll
-        for (int i = 0; i < NT; ++i) acc[j][i] = v4i{0, 0, 0, 0};
-    const auto get = [&](const int8_t *row, uint64_t at) {
+    const int8_t *b = p.b + (uint64_t)min(n0 + r, p.n - 1) * p.ldb;
+    const uint32_t steps = (p.k + 63) / 64, full = p.k / 64;
+    const uint32_t pitch = fused_pitch(p.k);
+
+    const auto get = [&](const int8_t *from, uint32_t step) {
+        const uint64_t at = (uint64_t)step * 64 + chunk * 16;
         v4i v = {0, 0, 0, 0};
         if (at + 16 <= p.k) {
-            __builtin_memcpy(&v, row + at, 16);
+            __builtin_memcpy(&v, from + at, 16);
         } else {
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-                if (at + e < p.k) v[e / 4] |= (int)((uint32_t)(uint8_t)row[at + e] << (8 * (e % 4)));
+                if (at + e < p.k) v[e / 4] |= (int)((uint32_t)(uint8_t)from[at + e] << (8 * (e % 4)));
         }
         return v;
     };
-    const uint32_t steps = (p.k + 63) / 64, full = p.k / 64;
-    uint32_t s = wave;
-    for (; s + (kUnroll - 1) * kWaves < full; s += kUnroll * kWaves) {
-        v4i fb[kUnroll][NT], fa[kUnroll][MT];
+    v4i fb[kAhead];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const uint64_t at = (uint64_t)(s + u * kWaves) * 64 + chunk * 16;
+    for (int u = 0; u < kAhead; ++u) {
+        const uint32_t step = wave + u * kWaves;
+        if (step < full) __builtin_memcpy(&fb[u], b + (uint64_t)step * 64 + chunk * 16, 16);
+    }
+
+    const int8_t *a[MT];
+    if constexpr (kFused) {
+        quantize_to_lds((const X *)p.a, p.lda, p.m, p.k, pitch, xq, sx, (uint32_t *)sums);
 #pragma unroll
-            for (int i = 0; i < NT; ++i) __builtin_memcpy(&fb[u][i], b[i] + at, 16);
+        for (int j = 0; j < MT; ++j) a[j] = xq + min(j * 16 + r, p.m - 1) * pitch;
+    } else {
 #pragma unroll
-            for (int j = 0; j < MT; ++j) __builtin_memcpy(&fa[u][j], a[j] + at, 16);
+        for (int j = 0; j < MT; ++j) a[j] = p.a + (uint64_t)min(j * 16 + r, p.m - 1) * p.lda;
+    }
+
+    v4i acc[MT];
+#pragma unroll
+    for (int j = 0; j < MT; ++j) acc[j] = v4i{0, 0, 0, 0};
+    const auto multiply = [&](const v4i &xb, uint32_t step) {
+        v4i fa[MT];
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+            if (kFused) fa[j] = *(const v4i *)(a[j] + step * 64 + chunk * 16);
+            else __builtin_memcpy(&fa[j], a[j] + (uint64_t)step * 64 + chunk * 16, 16);
         }
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
+        for (int j = 0; j < MT; ++j) acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(xb, fa[j], acc[j], 0, 0, 0);
+    };
+    uint32_t s = wave;
+    for (; s + (kAhead - 1) * kWaves < full; s += kAhead * kWaves) {
 #pragma unroll
-            for (int j = 0; j < MT; ++j)
-#pragma unroll
-                for (int i = 0; i < NT; ++i)
-                    acc[j][i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[u][i], fa[u][j], acc[j][i], 0, 0, 0);
+        for (int u = 0; u < kAhead; ++u) {
+            const v4i now = fb[u];
+            const uint32_t later = s + (kAhead + u) * kWaves;
+            if (later < full) __builtin_memcpy(&fb[u], b + (uint64_t)later * 64 + chunk * 16, 16);
+            multiply(now, s + u * kWaves);
+        }
     }
-    for (; s < steps; s += kWaves) {
-        const uint64_t at = (uint64_t)s * 64 + chunk * 16;
-        v4i fb[NT], fa[MT];
 #pragma unroll
-        for (int i = 0; i < NT; ++i) fb[i] = get(b[i], at);
+    for (int u = 0; u < kAhead; ++u)
+        if (s + u * kWaves < full) multiply(fb[u], s + u * kWaves);
+    if (full < steps && full % kWaves == wave) {  // the step that the end of k cuts
+        const v4i xb = get(b, full);
 #pragma unroll
-        for (int j = 0; j < MT; ++j) fa[j] = get(a[j], at);
-#pragma unroll
-        for (int j = 0; j < MT; ++j)
-#pragma unroll
-            for (int i = 0; i < NT; ++i)
-                acc[j][i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[i], fa[j], acc[j][i], 0, 0, 0);
+        for (int j = 0; j < MT; ++j) {
+            const v4i fa = kFused ? *(const v4i *)(a[j] + full * 64 + chunk * 16) : get(a[j], full);
+            acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(xb, fa, acc[j], 0, 0, 0);
+        }
     }
-    // lane: rows of y j * 16 + lane % 16, columns i * 16 + lane / 16 * 4 + e
+    // lane: rows of y j * 16 + lane % 16, columns lane / 16 * 4 + e
 #pragma unroll
-    for (int j = 0; j < MT; ++j)
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-            *(v4i *)&sums[wave][j * NT + i][lane * 4] = acc[j][i];
+    for (int j = 0; j < MT; ++j) *(v4i *)&sums[wave][j][lane * 4] = acc[j];
     __syncthreads();
-    for (uint32_t at = threadIdx.x; at < MT * NT * 256; at += 512) {
-        const uint32_t tile = at / 256, j = tile / NT, i = tile % NT, e = at % 256;
-        const uint32_t row = j * 16 + e / 4 % 16, col = n0 + i * 16 + e / 64 * 4 + e % 4;
+    for (uint32_t at = threadIdx.x; at < MT * 256; at += 512) {
+        const uint32_t j = at / 256, e = at % 256;
+        const uint32_t row = j * 16 + e / 4 % 16, col = n0 + e / 64 * 4 + e % 4;
         if (row >= p.m || col >= p.n) continue;
         int32_t sum = 0;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) sum += sums[w][tile][e];
-        ((OUT *)p.y)[(uint64_t)row * p.ldy + col] = (OUT)finish((float)sum, p.sa[row], p.sb, p.bias, col);
+        for (int w = 0; w < kWaves; ++w) sum += sums[w][j][e];
+        ((OUT *)p.y)[(uint64_t)row * p.ldy + col] =
+            (OUT)finish((float)sum, kFused ? sx[row] : p.sa[row], p.sb, p.bias, col);
     }
 }
 

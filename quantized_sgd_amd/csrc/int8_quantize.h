@@ -255,6 +255,47 @@ __global__ __launch_bounds__(256) void transpose_kernel(TransposeParams p) {
     }
 }
 
+// Bytes of a row of levels in LDS: whole 64-byte steps, and 16 more so that rows
+// begin in different banks.
+__host__ __device__ __forceinline__ uint32_t fused_pitch(uint32_t k) { return (k + 63) / 64 * 64 + 16; }
+
+// The levels of m rows of x into LDS and their scales into sx, by a workgroup of
+// eight waves; ends with a barrier. A row is taken by eight waves, or by fewer
+// where there are more rows. `part` holds 16 words.
+template <class X>
+__device__ __forceinline__ void quantize_to_lds(const X *x, uint64_t ldx, uint32_t m, uint32_t k, uint32_t pitch,
+                                                int8_t *levels, float *sx, uint32_t *part) {
+    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const uint32_t share = m == 1 ? 8 : m == 2 ? 4 : m <= 4 ? 2 : 1;  // waves of a row
+    const uint32_t at = wave % share * 512 + lane * 8, step = share * 512;
+    for (uint32_t r0 = 0; r0 < m; r0 += 8 / share) {
+        const uint32_t row = r0 + wave / share;
+        const X *from = x + (uint64_t)row * ldx;
+        uint32_t amax = 0;
+        if (row < m)
+            for (uint32_t c = at; c < k; c += step) {
+                float y[8];
+                load_upto8(from + c, (int64_t)k - c, 0.0f, y);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) amax = max(amax, magnitude(y[i]));
+            }
+        amax = wave_max(amax);
+        if (lane == 0) part[wave] = amax;
+        __syncthreads();
+        for (uint32_t i = 0; i < share; ++i) amax = max(amax, part[wave / share * share + i]);
+        const RowScale s = row_scale(amax);
+        if (row < m) {
+            if (at == 0) sx[row] = s.scale;
+            for (uint32_t c = at; c < pitch; c += step) {
+                float y[8] = {};
+                if (c < k) load_upto8(from + c, (int64_t)k - c, 0.0f, y);
+                put_levels(levels + (uint64_t)row * pitch, c, pitch, y, s);
+            }
+        }
+        __syncthreads();
+    }
+}
+
 // Copies rows of bytes to a row stride that is a multiple of 16, zeros past the
 // row's end, so that the product's tiles can be loaded 16 bytes at a time.
 struct RepackParams {

@@ -27,8 +27,8 @@ _teacher_p = ctypes.POINTER(_Teacher)
 
 
 @functools.lru_cache(maxsize=1024)
-def _workspace_bytes(rows, vocab):
-    return function("qsgd_distill_workspace", u64, u64, u64)(rows, vocab)
+def _workspace_bytes(rows, vocab, dtype):
+    return function("qsgd_distill_workspace", u64, u64, u64, _int)(rows, vocab, DTYPE[dtype])
 
 
 def _teacher(z, idx, t, tau, teacher_lse):
@@ -73,7 +73,7 @@ def distill_topk(z: torch.Tensor, idx: torch.Tensor, t: torch.Tensor, tau: float
     with on(dev, stream):
         loss = torch.empty(rows, dtype=torch.float32, device=dev)
         stats = torch.empty(rows, 4, dtype=torch.float32, device=dev)
-        ws = scratch(_workspace_bytes(rows, vocab), dev)
+        ws = scratch(_workspace_bytes(rows, vocab, z.dtype), dev)
         check(function("qsgd_distill_forward", _int, vp, _int, u64, u64, u64, _teacher_p, vp, vp, vp, vp)(
             z.data_ptr(), DTYPE[z.dtype], rows, vocab, ldz, te, loss.data_ptr(), stats.data_ptr(),
             None if ws is None else ws.data_ptr(), raw_stream(dev)), "qsgd_distill_forward")
@@ -112,7 +112,7 @@ def distill_topk_step(z: torch.Tensor, idx: torch.Tensor, t: torch.Tensor, grad_
     with on(dev, stream):
         out, ld = _gradient_out(z, ldz, out)
         loss = torch.empty(rows, dtype=torch.float32, device=dev)
-        ws = scratch(_workspace_bytes(rows, vocab), dev)
+        ws = scratch(_workspace_bytes(rows, vocab, z.dtype), dev)
         check(function("qsgd_distill_step", _int, vp, _int, u64, u64, u64, _teacher_p, vp, vp, vp, u64, vp, vp)(
             z.data_ptr(), DTYPE[z.dtype], rows, vocab, ldz, te, g, loss.data_ptr(), out.data_ptr(), ld,
             None if ws is None else ws.data_ptr(), raw_stream(dev)), "qsgd_distill_step")

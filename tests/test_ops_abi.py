@@ -56,7 +56,7 @@ def test_int8_argument_checks():
     assert size(16, 65536, 16, 65536, 64, 64, 65536) >= 2 * 64 * 64 * 4    # the sum is split
     lin = function("qsgd_int8_linear", i, vp, i, u64, vp, u64, vp, vp, vp, u64, vp, u64, vp, u64, u64, u64, vp, vp)
     assert lin(16, 0, 8, 16, 8, 16, None, 16, 5, None, 0, None, 0, 5, 8, None, None) == 0
-    assert lin(16, 0, 8, 16, 8, 16, None, 16, 5, None, 0, None, 4, 5, 8, None, None) == INVALID  # no workspace
+    assert lin(16, 0, 8, 16, 8, 16, None, 16, 5, None, 0, None, 40, 5, 8, None, None) == INVALID  # no workspace
     assert lin(16, 0, 8, 16, 8, 16, None, 16, 5, 16, 16, None, 4, 5, 8, None, None) == INVALID   # xq without sx
     assert lin(16, 0, 8, 16, 8, 16, None, 16, 5, 16, 8, 16, 4, 5, 8, None, None) == INVALID      # rows of xq not padded
     assert lin(16, 0, 8, 16, 8, 16, None, 16, 5, 24, 16, 16, 4, 5, 8, None, None) == INVALID     # xq not aligned
@@ -96,9 +96,9 @@ def test_distill_argument_checks():
     te = teacher()
     assert call(te, dtype=4) == INVALID and call(te, ldz=99) == INVALID and call(te, lddz=99) == INVALID
     assert call(te, z=None) == INVALID and call(te, loss=None) == INVALID and call(te, dz=None) == INVALID
-    size = function("qsgd_distill_workspace", u64, u64, u64)
-    assert size(4096, 131072) == 0 and size(0, 131072) == 0
-    assert size(2, 131072) > 0 and size(4096, 300000) > 0          # rows split into segments
+    size = function("qsgd_distill_workspace", u64, u64, u64, i)
+    assert size(4096, 131072, 0) == 0 and size(0, 131072, 0) == 0 and size(2, 131072, 3) == 0
+    assert size(2, 131072, 0) > 0 and size(4096, 300000, 2) > 0          # rows split into segments
     assert call(te, rows=2, vocab=131072, ldz=131072, lddz=131072) == INVALID  # no workspace
     back = function("qsgd_distill_backward", i, vp, i, u64, u64, u64, _teacher_p, vp, vp, vp, u64, vp)
     assert back(16, 0, 3, 100, 100, te, 8, None, 16, 100, None) == INVALID     # misaligned stats
