@@ -352,31 +352,6 @@ __global__ __launch_bounds__(kDT) void distill_row_kernel(DistillParams p) {
     if (GRAD) write_gradient<T>(p, row, 0, p.vocab, ts, st, e);
 }
 
-// The logits in a chunk's words.
-__device__ __forceinline__ void unpack(const uint32_t (&w)[8], float (&f)[8], float) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(w[j]);
-}
-__device__ __forceinline__ void unpack(const uint32_t (&w)[4], float (&f)[8], bf16) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        f[2 * j] = __uint_as_float(w[j] << 16);
-        f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-    }
-}
-__device__ __forceinline__ void unpack(const uint32_t (&w)[4], float (&f)[8], f16) {
-    typedef f16 pair __attribute__((ext_vector_type(2)));
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const pair v = __builtin_bit_cast(pair, w[j]);
-        f[2 * j] = (float)v[0];
-        f[2 * j + 1] = (float)v[1];
-    }
-}
-// Makes the compiler take a value as new, so that what it derived from it before
-// (here: the row in fp32) is not kept in registers for its next use.
-__device__ __forceinline__ void keep(uint32_t &v) { asm volatile("" : "+v"(v)); }
-
 // The same with the row held in registers: THREADS threads of NC chunks of eight
 // logits, and one entry a thread (k is at most THREADS). All loads are issued at
 // once, the entries' before the row's and the student's logits at the entries

@@ -39,27 +39,53 @@ qsgd_status quantize_rows(const void *x, qsgd_dtype dtype, uint64_t rows, uint64
     });
 }
 
-// Runs of rows for the column maxima: enough workgroups for the chip, at least 64
+// Runs of rows for the column maxima: enough workgroups for the chip, at least 32
 // rows each.
 uint32_t column_splits(uint64_t rows, uint64_t cols) {
-    const uint64_t blocks = div_up(cols, 512);
-    return (uint32_t)std::max<uint64_t>(1, std::min({(uint64_t)kMaxSplits, div_up(1024, blocks), div_up(rows, 64)}));
+    const uint64_t blocks = std::max<uint64_t>(1, div_up(cols, 512));
+    return (uint32_t)std::max<uint64_t>(1, std::min({(uint64_t)kMaxSplits, div_up(1024, blocks), div_up(rows, 32)}));
+}
+
+TransposeParams transpose_params(const void *x, uint64_t rows, uint64_t cols, uint64_t ldx, const float *fold,
+                                 int8_t *levels, uint64_t ldl, float *scale, uint64_t wide, void *workspace,
+                                 uint32_t splits) {
+    return {x, fold, levels, scale, (uint32_t *)workspace, ldx, ldl, (uint32_t)rows, (uint32_t)cols, (uint32_t)wide, splits,
+            (uint32_t)div_up(rows, splits), (uint32_t)std::max<uint64_t>(1, div_up(wide, 128)), (uint32_t)div_up(cols, 64)};
+}
+
+// The columns' scales from their runs' maxima, then the levels.
+template <class T>
+void launch_transpose(const TransposeParams &p, hipStream_t stream) {
+    column_scale_kernel<<<(uint32_t)div_up(p.cols, 64), 1024, 0, stream>>>(p);
+    if (p.wide) transpose_kernel<T><<<grid_of((uint64_t)p.row_tiles * p.col_tiles), 256, 0, stream>>>(p);
 }
 
 qsgd_status quantize_columns(const void *x, qsgd_dtype dtype, uint64_t rows, uint64_t cols, uint64_t ldx,
                              const float *fold, int8_t *levels, uint64_t ldl, float *scale, uint64_t wide,
                              void *workspace, hipStream_t stream) {
     if (cols == 0) return QSGD_OK;
-    const uint32_t splits = column_splits(rows, cols);
-    const uint32_t tr = (uint32_t)std::max<uint64_t>(1, div_up(wide, 128)), tc = (uint32_t)div_up(cols, 64);
+    const TransposeParams p =
+        transpose_params(x, rows, cols, ldx, fold, levels, ldl, scale, wide, workspace, column_splits(rows, cols));
     return with_type(dtype, [&](auto t) {
         using T = decltype(t);
-        const TransposeParams p{x, fold, levels, scale, (uint32_t *)workspace, ldx, ldl, (uint32_t)rows, (uint32_t)cols,
-                                (uint32_t)wide, splits, (uint32_t)div_up(rows, splits), tr, tc};
-        column_max_kernel<T><<<dim3((uint32_t)div_up(cols, 512), splits), 256, 0, stream>>>(p);
-        transpose_kernel<T><<<grid_of((uint64_t)tr * tc), 256, 0, stream>>>(p);
+        column_max_kernel<T><<<dim3((uint32_t)div_up(cols, 512), p.splits), 256, 0, stream>>>(p);
+        launch_transpose<T>(p, stream);
         return launched();
     });
+}
+
+// Rows and columns of x quantized together: their maxima in one pass where a row fits
+// a workgroup's registers.
+uint32_t both_splits(uint64_t rows) { return (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>(kMaxSplits, rows)); }
+bool takes_both(uint64_t rows, uint64_t cols) { return rows > 0 && cols > 0 && cols <= 8192; }
+
+template <class T>
+void launch_both(const QuantizeParams &q, const TransposeParams &p, hipStream_t stream) {
+    const uint32_t runs = p.splits;
+    if (q.wide <= 2048) quantize_both_kernel<T, 1><<<runs, 256, 0, stream>>>(q, p);
+    else if (q.wide <= 4096) quantize_both_kernel<T, 2><<<runs, 256, 0, stream>>>(q, p);
+    else quantize_both_kernel<T, 4><<<runs, 256, 0, stream>>>(q, p);
+    launch_transpose<T>(p, stream);
 }
 
 qsgd_status transpose_bytes(const int8_t *x, uint64_t rows, uint64_t cols, uint64_t ldx, int8_t *out, uint64_t ldo,
@@ -119,14 +145,21 @@ Plan plan_matmul(bool a_aligned, uint64_t lda, bool a_padded, bool b_aligned, ui
         p.at_b = p.bytes;
         p.bytes += round_up(n * kp, 256);
     }
+    // The tile: 64 x 64 up to two workgroups a CU (512 x 4096 x 4096: 15 us, 18 with
+    // 128 x 128; 2048^3, 1024 tiles: 16 us and 14), 256 x 256 once it fills most CUs
+    // (3000^3, 144 tiles: 46 us, 50 with 128 x 128; 2048 x 4096 x 4096, 128 tiles: 57
+    // and 41), else 128 x 128.
     const uint64_t side[3] = {64, 128, 256};
-    p.tile = 2;
-    while (p.tile > 0 && div_up(m, side[p.tile]) * div_up(n, side[p.tile]) < kCus * 3 / 4) --p.tile;
+    const auto tiles_of = [&](int tile) { return div_up(m, side[tile]) * div_up(n, side[tile]); };
+    p.tile = tiles_of(0) <= 2 * kCus ? 0 : tiles_of(2) >= 144 ? 2 : 1;
     p.tiles_m = div_up(m, side[p.tile]);
     p.tiles_n = div_up(n, side[p.tile]);
     const uint64_t tiles = p.tiles_m * p.tiles_n;
+    // The sum is split where it is long and tiles are few (64 x 512 x 8192, 8 tiles: 14
+    // us whole, 11 in 4 or 8 parts; 64 x 4096 x 4096, 64 tiles: 9 us whole, 11 in 2),
+    // and where it might pass 32 bits.
     uint64_t splits = div_up(all, kSafeSteps);
-    if (tiles < kCus) splits = std::max(splits, std::min({kCus / tiles, all / 4, (uint64_t)16}));
+    if (tiles <= 32) splits = std::max(splits, std::min(64 / tiles, all / 8));
     p.steps = div_up(all, splits);
     p.splits = div_up(all, p.steps);
     if (p.splits > 1) {
@@ -235,7 +268,7 @@ BackwardPlan plan_backward(uint64_t m, uint64_t n, uint64_t k) {
     b.hq = take(n * b.ldm);
     b.sh = take(4 * n);
     b.xt = take(k * b.ldm);
-    b.cols = take(qsgd_int8_quantize_transposed_workspace(m, n));
+    b.cols = take(4 * n * std::max(both_splits(m), column_splits(m, n)));
     b.own = take(std::max(b.gx.bytes, b.gw.bytes));
     b.bytes = at;
     return b;
@@ -342,20 +375,26 @@ qsgd_status qsgd_int8_linear_backward(const void *gy, qsgd_dtype dtype, uint64_t
     const BackwardPlan b = plan_backward(m, n, k);
     if (b.bytes && (!workspace || !aligned_to(workspace, 16))) return QSGD_ERR_INVALID_ARG;
     char *ws = (char *)workspace;
+    int8_t *gq = (int8_t *)(ws + b.gq), *wt = (int8_t *)(ws + b.wt), *hq = (int8_t *)(ws + b.hq), *xt = (int8_t *)(ws + b.xt);
+    float *sg = (float *)(ws + b.sg), *sh = (float *)(ws + b.sh);
+    const bool both = gx && gw && takes_both(m, n);
     qsgd_status st = QSGD_OK;
-    if (gx) {
-        int8_t *gq = (int8_t *)(ws + b.gq), *wt = (int8_t *)(ws + b.wt);
-        float *sg = (float *)(ws + b.sg);
-        st = quantize_rows(gy, dtype, m, n, ldgy, sw, gq, b.ldn, sg, b.ldn, stream);
+    if (both) {
+        st = with_type(dtype, [&](auto t) {
+            const QuantizeParams q{gy, sw, gq, sg, ldgy, b.ldn, (uint32_t)m, (uint32_t)n, (uint32_t)b.ldn};
+            launch_both<decltype(t)>(q, transpose_params(gy, m, n, ldgy, sx, hq, b.ldm, sh, b.ldm, ws + b.cols, both_splits(m)),
+                                     stream);
+            return launched();
+        });
+    }
+    if (st == QSGD_OK && gx) {
+        if (!both) st = quantize_rows(gy, dtype, m, n, ldgy, sw, gq, b.ldn, sg, b.ldn, stream);
         if (st == QSGD_OK) st = transpose_bytes(w, n, k, ldw, wt, b.ldn, b.ldn, stream);
         if (st == QSGD_OK)
             st = run_matmul(b.gx, gq, sg, wt, nullptr, nullptr, gx, dtype, ldgx, b.ldn, b.ldn, m, k, n, ws + b.own, stream);
-        if (st != QSGD_OK) return st;
     }
-    if (gw) {
-        int8_t *hq = (int8_t *)(ws + b.hq), *xt = (int8_t *)(ws + b.xt);
-        float *sh = (float *)(ws + b.sh);
-        st = quantize_columns(gy, dtype, m, n, ldgy, sx, hq, b.ldm, sh, b.ldm, ws + b.cols, stream);
+    if (st == QSGD_OK && gw) {
+        if (!both) st = quantize_columns(gy, dtype, m, n, ldgy, sx, hq, b.ldm, sh, b.ldm, ws + b.cols, stream);
         if (st == QSGD_OK) st = transpose_bytes(xq, m, k, ldxq, xt, b.ldm, b.ldm, stream);
         if (st == QSGD_OK)
             st = run_matmul(b.gw, hq, sh, xt, nullptr, nullptr, gw, QSGD_F32, ldgw, b.ldm, b.ldm, n, k, m, ws + b.own, stream);

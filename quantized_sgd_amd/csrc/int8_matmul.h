@@ -401,7 +401,7 @@ __global__ __launch_bounds__(256) void join_kernel(MatmulParams p) {
 }
 
 // Few rows of a: a workgroup of 8 waves takes 16 rows of b and all of k, its waves
-// every eighth 64-byte step. b goes from memory to registers in the matrix
+// every eighth 128 bytes of it. b goes from memory to registers in the matrix
 // instruction's own layout (16 bytes of a row a lane), at any alignment, kAhead
 // steps ahead; the rows of a, at most 16 MT, come from the caches. The waves' sums
 // meet in LDS.
@@ -435,12 +435,20 @@ __global__ __launch_bounds__(512) void skinny_kernel(MatmulParams p) {
         }
         return v;
     };
+    // steps of a wave: pairs, which are a cache line of each row, every eighth
+    const auto step_of = [&](uint32_t block, int u) { return block * (kAhead * kWaves) + (u / 2) * (2 * kWaves) + wave * 2 + u % 2; };
     v4i fb[kAhead];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-        const uint32_t step = wave + u * kWaves;
+        const uint32_t step = step_of(0, u);
         if (step < full) __builtin_memcpy(&fb[u], b + (uint64_t)step * 64 + chunk * 16, 16);
     }
+
+    // the scales of the element that this thread finishes, early
+    const uint32_t e = threadIdx.x % 256, row = threadIdx.x / 256 * 16 + e / 4 % 16, col = n0 + e / 64 * 4 + e % 4;
+    const bool mine = threadIdx.x < MT * 256 && row < p.m && col < p.n;
+    const float sb = mine && p.sb ? p.sb[col] : 1.0f, bias = mine && p.bias ? p.bias[col] : -0.0f;
+    const float sa = mine && !kFused ? p.sa[row] : 0.0f;
 
     const int8_t *a[MT];
     if constexpr (kFused) {
@@ -465,19 +473,21 @@ __global__ __launch_bounds__(512) void skinny_kernel(MatmulParams p) {
 #pragma unroll
         for (int j = 0; j < MT; ++j) acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(xb, fa[j], acc[j], 0, 0, 0);
     };
-    uint32_t s = wave;
-    for (; s + (kAhead - 1) * kWaves < full; s += kAhead * kWaves) {
+    uint32_t block = 0;
+    for (; (block + 1) * (kAhead * kWaves) <= full; ++block) {
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             const v4i now = fb[u];
-            const uint32_t later = s + (kAhead + u) * kWaves;
+            const uint32_t later = step_of(block + 1, u);
             if (later < full) __builtin_memcpy(&fb[u], b + (uint64_t)later * 64 + chunk * 16, 16);
-            multiply(now, s + u * kWaves);
+            multiply(now, step_of(block, u));
         }
     }
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u)
-        if (s + u * kWaves < full) multiply(fb[u], s + u * kWaves);
+    for (int u = 0; u < kAhead; ++u) {
+        const uint32_t step = step_of(block, u);
+        if (step < full) multiply(fb[u], step);
+    }
     if (full < steps && full % kWaves == wave) {  // the step that the end of k cuts
         const v4i xb = get(b, full);
 #pragma unroll
@@ -490,15 +500,11 @@ __global__ __launch_bounds__(512) void skinny_kernel(MatmulParams p) {
 #pragma unroll
     for (int j = 0; j < MT; ++j) *(v4i *)&sums[wave][j][lane * 4] = acc[j];
     __syncthreads();
-    for (uint32_t at = threadIdx.x; at < MT * 256; at += 512) {
-        const uint32_t j = at / 256, e = at % 256;
-        const uint32_t row = j * 16 + e / 4 % 16, col = n0 + e / 64 * 4 + e % 4;
-        if (row >= p.m || col >= p.n) continue;
+    if (mine) {
         int32_t sum = 0;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) sum += sums[w][j][e];
-        ((OUT *)p.y)[(uint64_t)row * p.ldy + col] =
-            (OUT)finish((float)sum, kFused ? sx[row] : p.sa[row], p.sb, p.bias, col);
+        for (int w = 0; w < kWaves; ++w) sum += sums[w][threadIdx.x / 256][e];
+        ((OUT *)p.y)[(uint64_t)row * p.ldy + col] = (OUT)((float)sum * (kFused ? sx[row] : sa) * sb + bias);
     }
 }
 

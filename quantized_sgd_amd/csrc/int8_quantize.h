@@ -23,29 +23,45 @@ struct RowScale {
     bool safe;  // y * inv is near y / scale
 };
 
+__device__ __forceinline__ RowScale with_inverse(float2 v) {
+    return {v.x, v.y, v.x > 0.0f && v.x < INFINITY, v.x > 0x1p-100f && v.x < 0x1p100f};
+}
 __device__ __forceinline__ RowScale row_scale(uint32_t amax) {
-    RowScale r;
-    r.scale = __uint_as_float(amax) / 127.0f;
-    r.ok = r.scale > 0.0f && r.scale < INFINITY;
-    r.safe = r.scale > 0x1p-100f && r.scale < 0x1p100f;
-    r.inv = 1.0f / r.scale;
-    return r;
+    const float scale = __uint_as_float(amax) / 127.0f;
+    return with_inverse(make_float2(scale, 1.0f / scale));
 }
 
-// RNE(RN32(y / scale)) without a division where it cannot matter. y * inv lies
-// within 127 * 2^-23 < 2e-5 of the real quotient (two roundings), RN32(y / scale)
-// within half of that, so they round to the same integer unless y * inv is within
-// 1e-4 of a half; then the quotient itself is taken. About one value in 5000
-// takes it with fp32 inputs.
-__device__ __forceinline__ int level_of(float y, const RowScale &s) {
-    float r = y * s.inv, k = rintf(r);
-    if (!s.safe || fabsf(fabsf(r - k) - 0.5f) < 1e-4f) k = rintf(y / s.scale);
-    k = fminf(fmaxf(k, -127.0f), 127.0f);  // a subnormal scale may be far below max |y| / 127
-    return s.ok ? (int)k : 0;
-}
-
-__device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d) {
-    return (uint32_t)(a & 255) | (uint32_t)(b & 255) << 8 | (uint32_t)(c & 255) << 16 | (uint32_t)d << 24;
+// Eight levels RNE(RN32(y / scale)), packed, without a division where it cannot
+// matter. y * inv lies within 127 * 2^-23 < 2e-5 of the real quotient (two
+// roundings), RN32(y / scale) within half of that, so they round to the same integer
+// unless y * inv is within 1e-4 of a half; then the quotient itself is taken.
+// Adding 1.5 * 2^23 rounds to the nearest integer (ties to even) and leaves its two's
+// complement in the sum's low bits, so a level costs five operations and three
+// byte permutes for four of them pack it. A safe scale is max |y| / 127 to 2^-24, so no
+// level passes 127; an unsafe one (subnormal) may be far from it.
+// The first four have scale s[0], the others s[1].
+__device__ __forceinline__ void levels8(const float (&y)[8], const RowScale (&s)[2], uint32_t (&w)[2]) {
+    constexpr float kMagic = 12582912.0f;
+    float b[8], d[8], far = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float r = y[i] * s[i / 4].inv;
+        b[i] = r + kMagic;
+        d[i] = r - (b[i] - kMagic);
+        far = fmaxf(far, fabsf(d[i]));
+    }
+    if (far > 0.4999f || !s[0].safe || !s[1].safe) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (fabsf(d[i]) > 0.4999f || !s[i / 4].safe)
+                b[i] = fminf(fmaxf(rintf(y[i] / s[i / 4].scale), -127.0f), 127.0f) + kMagic;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t lo = __builtin_amdgcn_perm(__float_as_uint(b[4 * h + 1]), __float_as_uint(b[4 * h]), 0x0c0c0400u);
+        const uint32_t hi = __builtin_amdgcn_perm(__float_as_uint(b[4 * h + 3]), __float_as_uint(b[4 * h + 2]), 0x0c0c0400u);
+        w[h] = s[h].ok ? lo | hi << 16 : 0u;
+    }
 }
 
 struct QuantizeParams {
@@ -61,17 +77,31 @@ struct QuantizeParams {
 // Eight levels to columns [c, c + 8) of a row, those below `wide`.
 __device__ __forceinline__ void put_levels(int8_t *row, uint32_t c, uint32_t wide, const float (&y)[8],
                                            const RowScale &s) {
-    int k[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) k[i] = level_of(y[i], s);
+    uint32_t w[2];
+    levels8(y, {s, s}, w);
     if (c + 8 <= wide) {
-        const uint32_t w[2] = {pack4(k[0], k[1], k[2], k[3]), pack4(k[4], k[5], k[6], k[7])};
         __builtin_memcpy(row + c, w, 8);
     } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (c + i < wide) row[c + i] = (int8_t)k[i];
+        for (uint32_t i = 0; c + i < wide; ++i) row[c + i] = (int8_t)((i < 4 ? w[0] : w[1]) >> (8 * (i & 3)));
     }
+}
+
+// Eight values of a row, 0 past its end, times their factors.
+template <class T>
+__device__ __forceinline__ void get_values(const T *x, const float *fold, uint32_t c, uint32_t cols, float (&y)[8]) {
+    load_upto8(x + c, (int64_t)cols - c, 0.0f, y);
+    if (fold) {
+        float f[8];
+        load_upto8(fold + c, (int64_t)cols - c, 0.0f, f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] *= f[i];
+    }
+}
+
+__device__ __forceinline__ uint32_t largest(uint32_t amax, const float (&y)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) amax = max(max(amax, magnitude(y[i])), magnitude(y[i + 1]));
+    return amax;
 }
 
 // TPR threads take a row (a wave or the workgroup), each NV chunks of 8 values
@@ -83,15 +113,7 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(QuantizeParams p) {
     const uint32_t t = threadIdx.x % TPR;
     if (row >= p.rows) return;  // a whole wave, or the workgroup
     const T *x = (const T *)p.x + (uint64_t)row * p.ldx;
-    const auto get = [&](uint32_t c, float (&y)[8]) {
-        load_upto8(x + c, (int64_t)p.cols - c, 0.0f, y);
-        if (p.fold) {
-            float f[8];
-            load_upto8(p.fold + c, (int64_t)p.cols - c, 0.0f, f);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] *= f[i];
-        }
-    };
+    const auto get = [&](uint32_t c, float (&y)[8]) { get_values(x, p.fold, c, p.cols, y); };
     uint32_t amax = 0;
     float y[NV > 0 ? NV : 1][8];
     if (NV > 0) {
@@ -100,14 +122,12 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(QuantizeParams p) {
             const uint32_t c = (v * TPR + t) * 8;
             if (c < p.cols) get(c, y[v]);
             else for (int i = 0; i < 8; ++i) y[v][i] = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) amax = max(amax, magnitude(y[v][i]));
+            amax = largest(amax, y[v]);
         }
     } else {
         for (uint64_t c = t * 8; c < p.cols; c += TPR * 8) {
             get((uint32_t)c, y[0]);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) amax = max(amax, magnitude(y[0][i]));
+            amax = largest(amax, y[0]);
         }
     }
     amax = wave_max(amax);
@@ -147,7 +167,7 @@ struct TransposeParams {
     uint32_t row_tiles, col_tiles;
 };
 
-constexpr uint32_t kMaxSplits = 32;
+constexpr uint32_t kMaxSplits = 512;
 
 // Column maxima of a run of rows: a wave takes every fourth row, a lane 8 columns.
 template <class T>
@@ -182,6 +202,119 @@ __global__ __launch_bounds__(256) void column_max_kernel(TransposeParams p) {
     }
 }
 
+// Row levels and column maxima in one pass over x, for the gradient, which needs x
+// quantized both ways: a workgroup takes a run of rows, a thread the same NV chunks
+// of columns of each, whose maxima it keeps. Rows go in groups of kGroup, the next
+// group's loads under this one's work; a group is held as it was loaded, so its
+// values are unpacked once for the maxima and once for the levels. `q` is the rows'
+// quantization (its fold goes along the columns), p.fold the factors of the rows for
+// the columns' maxima.
+template <class T, int NV>
+__global__ __launch_bounds__(256) void quantize_both_kernel(QuantizeParams q, TransposeParams p) {
+    constexpr int kWords = 2 * sizeof(T);
+    constexpr int kGroup = NV * (int)sizeof(T) <= 4 ? 4 : NV * (int)sizeof(T) <= 8 ? 2 : 1;
+    typedef uint32_t Group[kGroup][NV][kWords];
+    __shared__ uint32_t part[2][kGroup][4];
+    const uint32_t lo = blockIdx.x * p.rows_per_split, hi = min(p.rows, lo + p.rows_per_split);
+    if (lo >= hi) {
+        for (uint32_t c = threadIdx.x; c < p.cols; c += 256) p.part[(uint64_t)blockIdx.x * p.cols + c] = 0;
+        return;
+    }
+    uint32_t cmax[NV][8] = {};
+    float fold[NV][8];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        const uint32_t c = (v * 256 + threadIdx.x) * 8;
+        for (int i = 0; i < 8; ++i) fold[v][i] = 0.0f;
+        if (c < p.cols) load_upto8(q.fold + c, (int64_t)p.cols - c, 0.0f, fold[v]);
+    }
+    const auto get = [&](uint32_t r, Group &x) __attribute__((always_inline)) {
+#pragma unroll
+        for (int g = 0; g < kGroup; ++g) {
+            const T *from = (const T *)q.x + (uint64_t)min(r + g, hi - 1) * q.ldx;  // a row past the run: the last again
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                const uint32_t c = (v * 256 + threadIdx.x) * 8;
+                load_words(from + c, (int)min((int64_t)8, (int64_t)p.cols - c), x[g][v]);
+            }
+        }
+    };
+    const auto work = [&](uint32_t r, Group &x, uint32_t (&w)[kGroup][4]) __attribute__((always_inline)) {
+#pragma unroll
+        for (int g = 0; g < kGroup; ++g) {
+            const float f = p.fold[min(r + g, hi - 1)];
+            uint32_t amax = 0;
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                float y[8];
+                unpack(x[g][v], y, T{});
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    cmax[v][i] = max(cmax[v][i], magnitude(y[i] * f));
+                    y[i] *= fold[v][i];
+                }
+                amax = largest(amax, y);
+            }
+            amax = wave_max(amax);  // also keeps the rows apart: their values would fill the registers
+            if ((threadIdx.x & 63) == 0) w[g][threadIdx.x >> 6] = amax;
+        }
+        __syncthreads();  // w is next written two groups on, behind the next group's barrier
+#pragma unroll
+        for (int g = 0; g < kGroup; ++g) {
+            if (r + g >= hi) break;
+            const RowScale s = row_scale(max(max(w[g][0], w[g][1]), max(w[g][2], w[g][3])));
+            if (threadIdx.x == 0) q.scale[r + g] = s.scale;
+            int8_t *out = q.levels + (uint64_t)(r + g) * q.ldl;
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                const uint32_t c = (v * 256 + threadIdx.x) * 8;
+                float y[8];
+#pragma unroll
+                for (int i = 0; i < kWords; ++i) keep(x[g][v][i]);
+                unpack(x[g][v], y, T{});
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[i] *= fold[v][i];
+                if (c < q.wide) put_levels(out, c, q.wide, y, s);
+            }
+        }
+    };
+    Group x0, x1;
+    get(lo, x0);
+    for (uint32_t r = lo; r < hi; r += 2 * kGroup) {
+        get(r + kGroup, x1);
+        work(r, x0, part[0]);
+        if (r + kGroup >= hi) break;
+        get(r + 2 * kGroup, x0);
+        work(r + kGroup, x1, part[1]);
+    }
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t c = (v * 256 + threadIdx.x) * 8 + i;
+            if (c < p.cols) p.part[(uint64_t)blockIdx.x * p.cols + c] = cmax[v][i];
+        }
+}
+
+// Joins the runs' column maxima: a column's scale. 64 columns a workgroup, sixteen
+// threads a column.
+static __global__ __launch_bounds__(1024) void column_scale_kernel(TransposeParams p) {
+    __shared__ uint32_t part[16][64];
+    const uint32_t c = blockIdx.x * 64 + (threadIdx.x & 63), g = threadIdx.x >> 6;
+    uint32_t m = 0;
+    if (c < p.cols) {
+#pragma unroll 8
+        for (uint32_t s = g; s < p.splits; s += 16) m = max(m, p.part[(uint64_t)s * p.cols + c]);
+    }
+    part[g][threadIdx.x & 63] = m;
+    __syncthreads();
+    if (g == 0 && c < p.cols) {
+#pragma unroll
+        for (int i = 1; i < 16; ++i) m = max(m, part[i][threadIdx.x]);
+        p.scale[c] = row_scale(m).scale;
+    }
+}
+
 // A tile of 128 rows and 64 columns, transposed through LDS. A thread takes four
 // rows of eight columns, so a column's four levels make one LDS word: the tile's
 // columns have 33 words, which spreads a wave's writes over all banks. T = int8_t
@@ -190,19 +323,12 @@ template <class T>
 __global__ __launch_bounds__(256) void transpose_kernel(TransposeParams p) {
     constexpr bool kBytes = sizeof(T) == 1;
     __shared__ uint32_t tile[64 * 33];
-    __shared__ uint32_t cmax[4][64];
+    __shared__ float2 scales[64];  // with its inverse
     const uint32_t t = threadIdx.x;
     const uint64_t block = block_index();
     if (block >= (uint64_t)p.row_tiles * p.col_tiles) return;
     const uint32_t r0 = (uint32_t)(block % p.row_tiles) * 128, c0 = (uint32_t)(block / p.row_tiles) * 64;
     const uint32_t c = c0 + (t & 7) * 8, r = r0 + (t >> 3) * 4;
-    if (!kBytes) {
-        const uint32_t cc = c0 + (t & 63);
-        uint32_t m = 0;
-        if (cc < p.cols)
-            for (uint32_t s = t >> 6; s < p.splits; s += 4) m = max(m, p.part[(uint64_t)s * p.cols + cc]);
-        cmax[t >> 6][t & 63] = m;
-    }
     float y[4][8];
     uint8_t b[4][8];
 #pragma unroll
@@ -221,19 +347,27 @@ __global__ __launch_bounds__(256) void transpose_kernel(TransposeParams p) {
             for (int i = 0; i < 8; ++i) y[j][i] *= f;
         }
     }
-    __syncthreads();
+    if (kBytes) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t k = (t & 7) * 8 + i;
-        uint32_t w;
-        if (kBytes) {
-            w = pack4(b[0][i], b[1][i], b[2][i], b[3][i]);
-        } else {
-            const RowScale s = row_scale(max(max(cmax[0][k], cmax[1][k]), max(cmax[2][k], cmax[3][k])));
-            if (r0 == 0 && t < 8 && c + i < p.cols) p.scale[c + i] = s.scale;
-            w = pack4(level_of(y[0][i], s), level_of(y[1][i], s), level_of(y[2][i], s), level_of(y[3][i], s));
+        for (int i = 0; i < 8; ++i)
+            tile[((t & 7) * 8 + i) * 33 + (t >> 3)] =
+                (uint32_t)b[0][i] | (uint32_t)b[1][i] << 8 | (uint32_t)b[2][i] << 16 | (uint32_t)b[3][i] << 24;
+    } else {
+        if (t < 64) {
+            const float s = c0 + t < p.cols ? p.scale[c0 + t] : 0.0f;
+            scales[t] = make_float2(s, 1.0f / s);
         }
-        tile[k * 33 + (t >> 3)] = w;
+        __syncthreads();
+        // two columns at a time: four levels of each
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+            const uint32_t k = (t & 7) * 8 + i;
+            uint32_t w[2];
+            levels8({y[0][i], y[1][i], y[2][i], y[3][i], y[0][i + 1], y[1][i + 1], y[2][i + 1], y[3][i + 1]},
+                    {with_inverse(scales[k]), with_inverse(scales[k + 1])}, w);
+            tile[k * 33 + (t >> 3)] = w[0];
+            tile[(k + 1) * 33 + (t >> 3)] = w[1];
+        }
     }
     __syncthreads();
 #pragma unroll
@@ -276,8 +410,7 @@ __device__ __forceinline__ void quantize_to_lds(const X *x, uint64_t ldx, uint32
             for (uint32_t c = at; c < k; c += step) {
                 float y[8];
                 load_upto8(from + c, (int64_t)k - c, 0.0f, y);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) amax = max(amax, magnitude(y[i]));
+                amax = largest(amax, y);
             }
         amax = wave_max(amax);
         if (lane == 0) part[wave] = amax;

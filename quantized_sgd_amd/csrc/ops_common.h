@@ -26,7 +26,45 @@ __device__ __forceinline__ void load8(const T *p, float (&f)[8]) {
     for (int i = 0; i < 8; ++i) f[i] = (float)v[i];
 }
 
-// The same, of which only `count` elements (below 8, possibly none) exist; the
+// Eight elements that were loaded as words.
+__device__ __forceinline__ void unpack(const uint32_t (&w)[8], float (&f)[8], float) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(w[j]);
+}
+__device__ __forceinline__ void unpack(const uint32_t (&w)[4], float (&f)[8], bf16) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        f[2 * j] = __uint_as_float(w[j] << 16);
+        f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ void unpack(const uint32_t (&w)[4], float (&f)[8], f16) {
+    typedef f16 pair __attribute__((ext_vector_type(2)));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const pair v = __builtin_bit_cast(pair, w[j]);
+        f[2 * j] = (float)v[0];
+        f[2 * j + 1] = (float)v[1];
+    }
+}
+
+// Eight elements as words, those past the `count` there are as 0.
+template <class T>
+__device__ __forceinline__ void load_words(const T *p, int count, uint32_t (&w)[2 * sizeof(T)]) {
+    if (count >= 8) {
+        __builtin_memcpy(w, p, sizeof(w));
+    } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = i < count ? ((const uint32_t *)p)[i] : 0u;
+    } else {
+        const uint16_t *h = (const uint16_t *)p;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i] = (2 * i < count ? (uint32_t)h[2 * i] : 0u) | (2 * i + 1 < count ? (uint32_t)h[2 * i + 1] << 16 : 0u);
+    }
+}
+
+// load8, of which only `count` elements (below 8, possibly none) exist; the
 // others read as `fill`.
 template <class T>
 __device__ __forceinline__ void load_part(const T *p, int count, float fill, float (&f)[8]) {
@@ -39,6 +77,10 @@ __device__ __forceinline__ void load_upto8(const T *p, int64_t left, float fill,
     if (left >= 8) load8(p, f);
     else load_part(p, (int)left, fill, f);
 }
+
+// Makes the compiler take a value as new, so that what it derived from it before
+// (here: the row in fp32) is not kept in registers for its next use.
+__device__ __forceinline__ void keep(uint32_t &v) { asm volatile("" : "+v"(v)); }
 
 // Two at a time: gfx950 rounds a pair to bfloat16 in one instruction.
 template <class T>

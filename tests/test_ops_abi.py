@@ -68,6 +68,24 @@ def test_int8_argument_checks():
     assert back(16, 0, 5, 16, 8, 16, 16, 8, 16, 16, 7, 16, 8, 4, 5, 8, 16, None) == INVALID
 
 
+def test_workspaces_of_empty_sizes():
+    from quantized_sgd_amd._ops import function, u64, vp
+    import ctypes
+    back = function("qsgd_int8_linear_backward_workspace", u64, u64, u64, u64)
+    linear = function("qsgd_int8_linear_workspace", u64, vp, u64, u64, u64, u64, ctypes.c_int)
+    matmul = function("qsgd_int8_matmul_workspace", u64, vp, u64, vp, u64, u64, u64, u64)
+    columns = function("qsgd_int8_quantize_transposed_workspace", u64, u64, u64)
+    distill = function("qsgd_distill_workspace", u64, u64, u64, ctypes.c_int)
+    sizes = (0, 1, 40, 5000)
+    for m in sizes:
+        for n in sizes:
+            assert columns(m, n) >= 0 and distill(m, n, 0) >= 0
+            for k in sizes:
+                for keep in (0, 1):
+                    assert linear(16, max(k, 1), m, n, k, keep) >= 0
+                assert back(m, n, k) >= 0 and matmul(16, max(k, 1), 16, max(k, 1), m, n, k) >= 0
+
+
 def test_bindings_refuse_host_tensors():
     with pytest.raises(ValueError):
         q.int8_quantize(torch.zeros(2, 3))
