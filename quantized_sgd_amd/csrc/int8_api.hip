@@ -46,46 +46,21 @@ uint32_t column_splits(uint64_t rows, uint64_t cols) {
     return (uint32_t)std::max<uint64_t>(1, std::min({(uint64_t)kMaxSplits, div_up(1024, blocks), div_up(rows, 32)}));
 }
 
-TransposeParams transpose_params(const void *x, uint64_t rows, uint64_t cols, uint64_t ldx, const float *fold,
-                                 int8_t *levels, uint64_t ldl, float *scale, uint64_t wide, void *workspace,
-                                 uint32_t splits) {
-    return {x, fold, levels, scale, (uint32_t *)workspace, ldx, ldl, (uint32_t)rows, (uint32_t)cols, (uint32_t)wide, splits,
-            (uint32_t)div_up(rows, splits), (uint32_t)std::max<uint64_t>(1, div_up(wide, 128)), (uint32_t)div_up(cols, 64)};
-}
-
-// The columns' scales from their runs' maxima, then the levels.
-template <class T>
-void launch_transpose(const TransposeParams &p, hipStream_t stream) {
-    column_scale_kernel<<<(uint32_t)div_up(p.cols, 64), 1024, 0, stream>>>(p);
-    if (p.wide) transpose_kernel<T><<<grid_of((uint64_t)p.row_tiles * p.col_tiles), 256, 0, stream>>>(p);
-}
-
 qsgd_status quantize_columns(const void *x, qsgd_dtype dtype, uint64_t rows, uint64_t cols, uint64_t ldx,
                              const float *fold, int8_t *levels, uint64_t ldl, float *scale, uint64_t wide,
                              void *workspace, hipStream_t stream) {
     if (cols == 0) return QSGD_OK;
-    const TransposeParams p =
-        transpose_params(x, rows, cols, ldx, fold, levels, ldl, scale, wide, workspace, column_splits(rows, cols));
+    const uint32_t splits = column_splits(rows, cols);
+    const uint32_t tr = (uint32_t)std::max<uint64_t>(1, div_up(wide, 128)), tc = (uint32_t)div_up(cols, 64);
     return with_type(dtype, [&](auto t) {
         using T = decltype(t);
-        column_max_kernel<T><<<dim3((uint32_t)div_up(cols, 512), p.splits), 256, 0, stream>>>(p);
-        launch_transpose<T>(p, stream);
+        const TransposeParams p{x, fold, levels, scale, (uint32_t *)workspace, ldx, ldl, (uint32_t)rows, (uint32_t)cols,
+                                (uint32_t)wide, splits, (uint32_t)div_up(rows, splits), tr, tc};
+        column_max_kernel<T><<<dim3((uint32_t)div_up(cols, 512), splits), 256, 0, stream>>>(p);
+        column_scale_kernel<<<(uint32_t)div_up(cols, 64), 1024, 0, stream>>>(p);
+        if (rows) transpose_kernel<T><<<grid_of((uint64_t)tr * tc), 256, 0, stream>>>(p);
         return launched();
     });
-}
-
-// Rows and columns of x quantized together: their maxima in one pass where a row fits
-// a workgroup's registers.
-uint32_t both_splits(uint64_t rows) { return (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>(kMaxSplits, rows)); }
-bool takes_both(uint64_t rows, uint64_t cols) { return rows > 0 && cols > 0 && cols <= 8192; }
-
-template <class T>
-void launch_both(const QuantizeParams &q, const TransposeParams &p, hipStream_t stream) {
-    const uint32_t runs = p.splits;
-    if (q.wide <= 2048) quantize_both_kernel<T, 1><<<runs, 256, 0, stream>>>(q, p);
-    else if (q.wide <= 4096) quantize_both_kernel<T, 2><<<runs, 256, 0, stream>>>(q, p);
-    else quantize_both_kernel<T, 4><<<runs, 256, 0, stream>>>(q, p);
-    launch_transpose<T>(p, stream);
 }
 
 qsgd_status transpose_bytes(const int8_t *x, uint64_t rows, uint64_t cols, uint64_t ldx, int8_t *out, uint64_t ldo,
@@ -268,7 +243,7 @@ BackwardPlan plan_backward(uint64_t m, uint64_t n, uint64_t k) {
     b.hq = take(n * b.ldm);
     b.sh = take(4 * n);
     b.xt = take(k * b.ldm);
-    b.cols = take(4 * n * std::max(both_splits(m), column_splits(m, n)));
+    b.cols = take(4 * n * column_splits(m, n));
     b.own = take(std::max(b.gx.bytes, b.gw.bytes));
     b.bytes = at;
     return b;
@@ -377,24 +352,15 @@ qsgd_status qsgd_int8_linear_backward(const void *gy, qsgd_dtype dtype, uint64_t
     char *ws = (char *)workspace;
     int8_t *gq = (int8_t *)(ws + b.gq), *wt = (int8_t *)(ws + b.wt), *hq = (int8_t *)(ws + b.hq), *xt = (int8_t *)(ws + b.xt);
     float *sg = (float *)(ws + b.sg), *sh = (float *)(ws + b.sh);
-    const bool both = gx && gw && takes_both(m, n);
     qsgd_status st = QSGD_OK;
-    if (both) {
-        st = with_type(dtype, [&](auto t) {
-            const QuantizeParams q{gy, sw, gq, sg, ldgy, b.ldn, (uint32_t)m, (uint32_t)n, (uint32_t)b.ldn};
-            launch_both<decltype(t)>(q, transpose_params(gy, m, n, ldgy, sx, hq, b.ldm, sh, b.ldm, ws + b.cols, both_splits(m)),
-                                     stream);
-            return launched();
-        });
-    }
     if (st == QSGD_OK && gx) {
-        if (!both) st = quantize_rows(gy, dtype, m, n, ldgy, sw, gq, b.ldn, sg, b.ldn, stream);
+        st = quantize_rows(gy, dtype, m, n, ldgy, sw, gq, b.ldn, sg, b.ldn, stream);
         if (st == QSGD_OK) st = transpose_bytes(w, n, k, ldw, wt, b.ldn, b.ldn, stream);
         if (st == QSGD_OK)
             st = run_matmul(b.gx, gq, sg, wt, nullptr, nullptr, gx, dtype, ldgx, b.ldn, b.ldn, m, k, n, ws + b.own, stream);
     }
     if (st == QSGD_OK && gw) {
-        if (!both) st = quantize_columns(gy, dtype, m, n, ldgy, sx, hq, b.ldm, sh, b.ldm, ws + b.cols, stream);
+        st = quantize_columns(gy, dtype, m, n, ldgy, sx, hq, b.ldm, sh, b.ldm, ws + b.cols, stream);
         if (st == QSGD_OK) st = transpose_bytes(xq, m, k, ldxq, xt, b.ldm, b.ldm, stream);
         if (st == QSGD_OK)
             st = run_matmul(b.gw, hq, sh, xt, nullptr, nullptr, gw, QSGD_F32, ldgw, b.ldm, b.ldm, n, k, m, ws + b.own, stream);

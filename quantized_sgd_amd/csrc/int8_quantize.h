@@ -86,18 +86,6 @@ __device__ __forceinline__ void put_levels(int8_t *row, uint32_t c, uint32_t wid
     }
 }
 
-// Eight values of a row, 0 past its end, times their factors.
-template <class T>
-__device__ __forceinline__ void get_values(const T *x, const float *fold, uint32_t c, uint32_t cols, float (&y)[8]) {
-    load_upto8(x + c, (int64_t)cols - c, 0.0f, y);
-    if (fold) {
-        float f[8];
-        load_upto8(fold + c, (int64_t)cols - c, 0.0f, f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] *= f[i];
-    }
-}
-
 __device__ __forceinline__ uint32_t largest(uint32_t amax, const float (&y)[8]) {
 #pragma unroll
     for (int i = 0; i < 8; i += 2) amax = max(max(amax, magnitude(y[i])), magnitude(y[i + 1]));
@@ -113,20 +101,39 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(QuantizeParams p) {
     const uint32_t t = threadIdx.x % TPR;
     if (row >= p.rows) return;  // a whole wave, or the workgroup
     const T *x = (const T *)p.x + (uint64_t)row * p.ldx;
-    const auto get = [&](uint32_t c, float (&y)[8]) { get_values(x, p.fold, c, p.cols, y); };
+    const auto values = [&](uint32_t c, Eight<T> &raw, Eight<float> &raw_fold, float (&y)[8]) {
+        settle(c, p.cols, raw, y);
+        if (p.fold) {
+            float f[8];
+            settle(c, p.cols, raw_fold, f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] *= f[i];
+        }
+    };
     uint32_t amax = 0;
     float y[NV > 0 ? NV : 1][8];
     if (NV > 0) {
+        Eight<T> raw[NV > 0 ? NV : 1];
+        Eight<float> raw_fold[NV > 0 ? NV : 1];
+#pragma unroll
+        for (int v = 0; v < NV; ++v) fetch(x, (v * TPR + t) * 8, p.cols, raw[v]);
+        if (p.fold) {
+#pragma unroll
+            for (int v = 0; v < NV; ++v) fetch(p.fold, (v * TPR + t) * 8, p.cols, raw_fold[v]);
+        }
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            const uint32_t c = (v * TPR + t) * 8;
-            if (c < p.cols) get(c, y[v]);
-            else for (int i = 0; i < 8; ++i) y[v][i] = 0.0f;
+            values((v * TPR + t) * 8, raw[v], raw_fold[v], y[v]);
             amax = largest(amax, y[v]);
         }
     } else {
-        for (uint64_t c = t * 8; c < p.cols; c += TPR * 8) {
-            get((uint32_t)c, y[0]);
+#pragma unroll 4
+        for (uint32_t c = t * 8; c < p.cols; c += TPR * 8) {
+            Eight<T> raw;
+            Eight<float> raw_fold;
+            fetch(x, c, p.cols, raw);
+            if (p.fold) fetch(p.fold, c, p.cols, raw_fold);
+            values(c, raw, raw_fold, y[0]);
             amax = largest(amax, y[0]);
         }
     }
@@ -146,10 +153,13 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(QuantizeParams p) {
             if (c < p.wide) put_levels(out, c, p.wide, y[v], s);
         }
     } else {
-        for (uint64_t c = t * 8; c < p.wide; c += TPR * 8) {
-            if (c < p.cols) get((uint32_t)c, y[0]);
-            else for (int i = 0; i < 8; ++i) y[0][i] = 0.0f;
-            put_levels(out, (uint32_t)c, p.wide, y[0], s);
+        for (uint32_t c = t * 8; c < p.wide; c += TPR * 8) {
+            Eight<T> raw;
+            Eight<float> raw_fold;
+            fetch(x, c, p.cols, raw);
+            if (p.fold) fetch(p.fold, c, p.cols, raw_fold);
+            values(c, raw, raw_fold, y[0]);
+            put_levels(out, c, p.wide, y[0], s);
         }
     }
 }
@@ -167,7 +177,7 @@ struct TransposeParams {
     uint32_t row_tiles, col_tiles;
 };
 
-constexpr uint32_t kMaxSplits = 512;
+constexpr uint32_t kMaxSplits = 256;
 
 // Column maxima of a run of rows: a wave takes every fourth row, a lane 8 columns.
 template <class T>
@@ -178,14 +188,24 @@ __global__ __launch_bounds__(256) void column_max_kernel(TransposeParams p) {
     const uint32_t lo = blockIdx.y * p.rows_per_split, hi = min(p.rows, lo + p.rows_per_split);
     uint32_t amax[8] = {};
     if (c < p.cols) {
-        const T *x = (const T *)p.x + c;
-#pragma unroll 4
-        for (uint32_t r = lo + wave; r < hi; r += 4) {
-            float y[8];
-            load_upto8(x + (uint64_t)r * p.ldx, (int64_t)p.cols - c, 0.0f, y);
-            const float f = p.fold ? p.fold[r] : 1.0f;
+        const T *x = (const T *)p.x;
+        constexpr int kRows = 4;  // loads in flight
+        for (uint32_t r = lo + wave; r < hi; r += 4 * kRows) {
+            Eight<T> raw[kRows];
+            float f[kRows];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) amax[i] = max(amax[i], magnitude(y[i] * f));
+            for (int g = 0; g < kRows; ++g) {
+                const uint32_t at = min(r + 4 * g, hi - 1);  // past the run: its last row again
+                fetch(x + (uint64_t)at * p.ldx, c, p.cols, raw[g]);
+                f[g] = p.fold ? p.fold[at] : 1.0f;
+            }
+#pragma unroll
+            for (int g = 0; g < kRows; ++g) {
+                float y[8];
+                settle(c, p.cols, raw[g], y);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) amax[i] = max(amax[i], magnitude(y[i] * f[g]));
+            }
         }
     }
     if (wave) {
@@ -200,100 +220,6 @@ __global__ __launch_bounds__(256) void column_max_kernel(TransposeParams p) {
             if (c + i < p.cols) p.part[(uint64_t)blockIdx.y * p.cols + c + i] = m;
         }
     }
-}
-
-// Row levels and column maxima in one pass over x, for the gradient, which needs x
-// quantized both ways: a workgroup takes a run of rows, a thread the same NV chunks
-// of columns of each, whose maxima it keeps. Rows go in groups of kGroup, the next
-// group's loads under this one's work; a group is held as it was loaded, so its
-// values are unpacked once for the maxima and once for the levels. `q` is the rows'
-// quantization (its fold goes along the columns), p.fold the factors of the rows for
-// the columns' maxima.
-template <class T, int NV>
-__global__ __launch_bounds__(256) void quantize_both_kernel(QuantizeParams q, TransposeParams p) {
-    constexpr int kWords = 2 * sizeof(T);
-    constexpr int kGroup = NV * (int)sizeof(T) <= 4 ? 4 : NV * (int)sizeof(T) <= 8 ? 2 : 1;
-    typedef uint32_t Group[kGroup][NV][kWords];
-    __shared__ uint32_t part[2][kGroup][4];
-    const uint32_t lo = blockIdx.x * p.rows_per_split, hi = min(p.rows, lo + p.rows_per_split);
-    if (lo >= hi) {
-        for (uint32_t c = threadIdx.x; c < p.cols; c += 256) p.part[(uint64_t)blockIdx.x * p.cols + c] = 0;
-        return;
-    }
-    uint32_t cmax[NV][8] = {};
-    float fold[NV][8];
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        const uint32_t c = (v * 256 + threadIdx.x) * 8;
-        for (int i = 0; i < 8; ++i) fold[v][i] = 0.0f;
-        if (c < p.cols) load_upto8(q.fold + c, (int64_t)p.cols - c, 0.0f, fold[v]);
-    }
-    const auto get = [&](uint32_t r, Group &x) __attribute__((always_inline)) {
-#pragma unroll
-        for (int g = 0; g < kGroup; ++g) {
-            const T *from = (const T *)q.x + (uint64_t)min(r + g, hi - 1) * q.ldx;  // a row past the run: the last again
-#pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                const uint32_t c = (v * 256 + threadIdx.x) * 8;
-                load_words(from + c, (int)min((int64_t)8, (int64_t)p.cols - c), x[g][v]);
-            }
-        }
-    };
-    const auto work = [&](uint32_t r, Group &x, uint32_t (&w)[kGroup][4]) __attribute__((always_inline)) {
-#pragma unroll
-        for (int g = 0; g < kGroup; ++g) {
-            const float f = p.fold[min(r + g, hi - 1)];
-            uint32_t amax = 0;
-#pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                float y[8];
-                unpack(x[g][v], y, T{});
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    cmax[v][i] = max(cmax[v][i], magnitude(y[i] * f));
-                    y[i] *= fold[v][i];
-                }
-                amax = largest(amax, y);
-            }
-            amax = wave_max(amax);  // also keeps the rows apart: their values would fill the registers
-            if ((threadIdx.x & 63) == 0) w[g][threadIdx.x >> 6] = amax;
-        }
-        __syncthreads();  // w is next written two groups on, behind the next group's barrier
-#pragma unroll
-        for (int g = 0; g < kGroup; ++g) {
-            if (r + g >= hi) break;
-            const RowScale s = row_scale(max(max(w[g][0], w[g][1]), max(w[g][2], w[g][3])));
-            if (threadIdx.x == 0) q.scale[r + g] = s.scale;
-            int8_t *out = q.levels + (uint64_t)(r + g) * q.ldl;
-#pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                const uint32_t c = (v * 256 + threadIdx.x) * 8;
-                float y[8];
-#pragma unroll
-                for (int i = 0; i < kWords; ++i) keep(x[g][v][i]);
-                unpack(x[g][v], y, T{});
-#pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] *= fold[v][i];
-                if (c < q.wide) put_levels(out, c, q.wide, y, s);
-            }
-        }
-    };
-    Group x0, x1;
-    get(lo, x0);
-    for (uint32_t r = lo; r < hi; r += 2 * kGroup) {
-        get(r + kGroup, x1);
-        work(r, x0, part[0]);
-        if (r + kGroup >= hi) break;
-        get(r + 2 * kGroup, x0);
-        work(r + kGroup, x1, part[1]);
-    }
-#pragma unroll
-    for (int v = 0; v < NV; ++v)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t c = (v * 256 + threadIdx.x) * 8 + i;
-            if (c < p.cols) p.part[(uint64_t)blockIdx.x * p.cols + c] = cmax[v][i];
-        }
 }
 
 // Joins the runs' column maxima: a column's scale. 64 columns a workgroup, sixteen
@@ -331,20 +257,29 @@ __global__ __launch_bounds__(256) void transpose_kernel(TransposeParams p) {
     const uint32_t c = c0 + (t & 7) * 8, r = r0 + (t >> 3) * 4;
     float y[4][8];
     uint8_t b[4][8];
+    if constexpr (kBytes) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const bool there = r + j < p.rows && c < p.cols;
-        const T *x = (const T *)p.x + (uint64_t)(r + j) * p.ldx + c;
-        if (kBytes) {
+        for (int j = 0; j < 4; ++j) {
+            const bool there = r + j < p.rows && c < p.cols;
+            const T *x = (const T *)p.x + (uint64_t)(r + j) * p.ldx + c;
             if (there && c + 8 <= p.cols) __builtin_memcpy(b[j], x, 8);
             else
                 for (int i = 0; i < 8; ++i) b[j][i] = there && c + i < p.cols ? (uint8_t)x[i] : 0;
-        } else {
-            if (there) load_upto8(x, (int64_t)p.cols - c, 0.0f, y[j]);
-            else for (int i = 0; i < 8; ++i) y[j][i] = 0.0f;
-            const float f = p.fold && there ? p.fold[r + j] : 1.0f;
+        }
+    } else {
+        Eight<T> raw[4];
+        float f[4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[j][i] *= f;
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t at = min(r + j, p.rows - 1);
+            fetch((const T *)p.x + (uint64_t)at * p.ldx, c, p.cols, raw[j]);
+            f[j] = p.fold ? p.fold[at] : 1.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            settle(c, p.cols, raw[j], y[j]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[j][i] = r + j < p.rows ? y[j][i] * f[j] : 0.0f;
         }
     }
     if (kBytes) {
@@ -409,7 +344,9 @@ __device__ __forceinline__ void quantize_to_lds(const X *x, uint64_t ldx, uint32
         if (row < m)
             for (uint32_t c = at; c < k; c += step) {
                 float y[8];
-                load_upto8(from + c, (int64_t)k - c, 0.0f, y);
+                Eight<X> raw;
+                fetch(from, c, k, raw);
+                settle(c, k, raw, y);
                 amax = largest(amax, y);
             }
         amax = wave_max(amax);
@@ -420,8 +357,10 @@ __device__ __forceinline__ void quantize_to_lds(const X *x, uint64_t ldx, uint32
         if (row < m) {
             if (at == 0) sx[row] = s.scale;
             for (uint32_t c = at; c < pitch; c += step) {
-                float y[8] = {};
-                if (c < k) load_upto8(from + c, (int64_t)k - c, 0.0f, y);
+                float y[8];
+                Eight<X> raw;
+                fetch(from, c, k, raw);
+                settle(c, k, raw, y);
                 put_levels(levels + (uint64_t)row * pitch, c, pitch, y, s);
             }
         }

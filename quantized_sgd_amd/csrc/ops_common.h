@@ -48,20 +48,39 @@ __device__ __forceinline__ void unpack(const uint32_t (&w)[4], float (&f)[8], f1
     }
 }
 
-// Eight elements as words, those past the `count` there are as 0.
+// Elements [c, c + 8) of a row of n, as words; those past its end are 0. In two
+// parts, so that a thread's loads can all be issued before the first is looked at:
+// fetch() loads eight elements that exist without a branch (the row's last ones
+// where c + 8 passes its end), settle() moves them to their places in the few
+// threads at the row's end.
 template <class T>
-__device__ __forceinline__ void load_words(const T *p, int count, uint32_t (&w)[2 * sizeof(T)]) {
-    if (count >= 8) {
-        __builtin_memcpy(w, p, sizeof(w));
-    } else if constexpr (sizeof(T) == 4) {
+struct Eight {
+    uint32_t w[2 * sizeof(T)];
+};
+template <class T>
+__device__ __forceinline__ void fetch(const T *row, uint32_t c, uint32_t n, Eight<T> &v) {
+    if (n >= 8) {
+        __builtin_memcpy(v.w, row + min(c, n - 8), sizeof(v.w));
+    } else {  // a row of a few elements
+        T e[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = i < count ? ((const uint32_t *)p)[i] : 0u;
-    } else {
-        const uint16_t *h = (const uint16_t *)p;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            w[i] = (2 * i < count ? (uint32_t)h[2 * i] : 0u) | (2 * i + 1 < count ? (uint32_t)h[2 * i + 1] << 16 : 0u);
+        for (int i = 0; i < 8; ++i) e[i] = (uint32_t)i < n ? row[i] : (T)0.0f;
+        __builtin_memcpy(v.w, e, sizeof(v.w));
     }
+}
+template <class T>
+__device__ __forceinline__ void settle(uint32_t c, uint32_t n, Eight<T> &v, float (&f)[8]) {
+    unpack(v.w, f, T{});
+    const uint32_t from = n >= 8 ? min(c, n - 8) : 0u;
+    if (c == from) return;
+    const uint32_t by = c - from;  // the elements before c
+#pragma unroll
+    for (int s = 1; s < 8; s *= 2) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = by & s ? (i + s < 8 ? f[i + s] : 0.0f) : f[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = by >= 8 ? 0.0f : f[i];
 }
 
 // load8, of which only `count` elements (below 8, possibly none) exist; the
