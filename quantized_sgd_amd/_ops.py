@@ -34,21 +34,24 @@ def check(status: int, what: str):
         raise QsgdError(status, what)
 
 
-def matrix(t: torch.Tensor, name: str, dtypes, rows=None, cols=None):
-    """A 2-D device tensor of one of `dtypes` (and of the given sizes) whose rows
-    are contiguous and do not overlap. Returns its row stride."""
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have two dimensions, got {t.dim()}")
+def matrix(t: torch.Tensor, name: str, dtypes, rows=None, cols=None, device=None):
+    """A 2-D device tensor of one of `dtypes` (of the given sizes, on the given
+    device) whose rows are contiguous and do not overlap. Returns its row stride."""
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must have two dimensions, got {len(shape)}")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be one of {', '.join(map(str, dtypes))}, got {t.dtype}")
-    r, c = t.shape
+    r, c = shape
     if (rows is not None and r != rows) or (cols is not None and c != cols):
         raise ValueError(f"{name} must be [{'any' if rows is None else rows}, {'any' if cols is None else cols}], "
                          f"got [{r}, {c}]")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} must be on {device}, is on {t.device}")
     ld, step = t.stride()
-    if c > 1 and step != 1:
+    if step != 1 and c > 1:
         raise ValueError(f"{name} must have contiguous rows")
     if r <= 1 or c == 0:
         return max(c, 1)
@@ -63,19 +66,14 @@ def vector(t, name: str, n: int, device, dtype=torch.float32):
         return None
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 1 or t.shape[0] != n:
-        raise ValueError(f"{name} must be [{n}], got {list(t.shape)}")
+    shape = t.shape
+    if len(shape) != 1 or shape[0] != n:
+        raise ValueError(f"{name} must be [{n}], got {list(shape)}")
     if t.device != device:
-        raise ValueError(f"{name} must be on {device}")
+        raise ValueError(f"{name} must be on {device}, is on {t.device}")
     if n > 1 and t.stride(0) != 1:
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
-
-
-def same_device(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} must be on {device}, is on {t.device}")
 
 
 _nothing = contextlib.nullcontext()

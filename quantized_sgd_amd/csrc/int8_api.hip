@@ -83,6 +83,15 @@ constexpr uint64_t kMaxK = 1u << 23;  // a tile's row offsets are 32-bit
 constexpr uint64_t kSafeSteps = 1023; // 128-byte steps whose sum of products stays below 2^31 (1023 * 128 * 128^2)
 constexpr uint64_t kCus = 256;
 
+// Few rows go through skinny_kernel, 16 columns a workgroup, but for wide layers of
+// more than 8 rows, which take the tiles (n x k, weights out of the last-level cache or,
+// marked *, out of memory; 1 row: 4096 x 4096, 6.4 us and 10.1; 16384 x 8192*, 28 and 33.
+// 16 rows: 4096 x 4096, 6.9 and 10.1; 8192 x 8192, 18.8 and 17.7; 16384 x 8192*, 38 and
+// 33. 32 rows: 4096 x 4096, 9.3 and 10.2; 8192 x 8192, 26.0 and 17.8).
+bool is_skinny(uint64_t m, uint64_t n) {
+    return n <= (1u << 24) && (m <= 8 || (m <= 16 && n <= 8192) || (m <= 32 && n <= 4096));
+}
+
 struct Plan {
     bool skinny = false;
     bool repack_a = false, repack_b = false;
@@ -102,8 +111,9 @@ Plan plan_matmul(bool a_aligned, uint64_t lda, bool a_padded, bool b_aligned, ui
     Plan p;
     p.lda = lda;
     p.ldb = ldb;
+    if (m == 0 || n == 0) return p;  // nothing is launched
     const uint64_t all = std::max<uint64_t>(1, div_up(k, 128));
-    if (m <= 32 && n <= (1u << 24) && all <= kSafeSteps) {
+    if (is_skinny(m, n) && all <= kSafeSteps) {
         p.skinny = true;
         return p;
     }
@@ -207,11 +217,9 @@ Plan plan_of(const int8_t *a, uint64_t lda, bool a_padded, const int8_t *b, uint
     return plan_matmul(aligned_to(a, 16), lda, a_padded, aligned_to(b, 16), ldb, false, m, n, k);
 }
 
-// The layer in one launch: the rows' levels fit 32 KB of LDS (every workgroup makes
-// them for itself) and nobody keeps them.
-bool fuses(uint64_t m, uint64_t n, uint64_t k) {
-    return m <= 16 && n > 0 && n <= (1u << 24) && k <= 32768 && m * fused_pitch((uint32_t)k) <= 32768;
-}
+// The layer in one launch: every workgroup can hold the rows (at most 8), and nobody
+// keeps their levels.
+bool fuses(uint64_t m, uint64_t n, uint64_t k) { return n > 0 && k > 0 && is_skinny(m, n) && holds_rows(m, k); }
 
 bool dims_ok(uint64_t m, uint64_t n, uint64_t k) { return m <= kMaxDim && n <= kMaxDim && k <= kMaxDim; }
 

@@ -8,6 +8,8 @@
 //  - skinny_kernel: few rows of a (single tokens), bound by reading b once.
 #pragma once
 
+#include <type_traits>
+
 #include "int8_quantize.h"
 #include "ops_common.h"
 
@@ -408,14 +410,15 @@ __global__ __launch_bounds__(256) void join_kernel(MatmulParams p) {
 //
 // X = int8_t: a is quantized. Otherwise a is the layer's input and every workgroup
 // quantizes it into LDS for itself, while its first steps of b are on their way:
-// for the few rows this is made for that costs less than a launch.
+// for the few rows that its registers hold that costs less than a launch (one
+// token through 4096 x 4096: 7.8 us, 7.0 + 3.6 in two launches).
 template <int MT, class X, class OUT>
-__global__ __launch_bounds__(512) void skinny_kernel(MatmulParams p) {
+__global__ __launch_bounds__(512, 4) void skinny_kernel(MatmulParams p) {
     constexpr int kWaves = 8, kAhead = 8;
     constexpr bool kFused = sizeof(X) > 1;
     extern __shared__ __align__(16) int8_t xq[];  // kFused: [m, pitch]
     __shared__ __align__(16) int32_t sums[kWaves][MT][256];
-    __shared__ float sx[kFused ? 16 * MT : 1];
+    __shared__ float sx[8];
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const uint32_t n0 = blockIdx.x * 16;
     const uint32_t r = lane & 15, chunk = lane >> 4;
@@ -437,6 +440,8 @@ __global__ __launch_bounds__(512) void skinny_kernel(MatmulParams p) {
     };
     // steps of a wave: pairs, which are a cache line of each row, every eighth
     const auto step_of = [&](uint32_t block, int u) { return block * (kAhead * kWaves) + (u / 2) * (2 * kWaves) + wave * 2 + u % 2; };
+    HeldRow<typename std::conditional<kFused, X, float>::type> held;  // loads return in order: a's before b's
+    if constexpr (kFused) load_row((const X *)p.a, p.lda, p.m, p.k, held);
     v4i fb[kAhead];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
@@ -452,7 +457,7 @@ __global__ __launch_bounds__(512) void skinny_kernel(MatmulParams p) {
 
     const int8_t *a[MT];
     if constexpr (kFused) {
-        quantize_to_lds((const X *)p.a, p.lda, p.m, p.k, pitch, xq, sx, (uint32_t *)sums);
+        quantize_to_lds(held, p.m, p.k, pitch, xq, sx, (uint32_t *)sums);
 #pragma unroll
         for (int j = 0; j < MT; ++j) a[j] = xq + min(j * 16 + r, p.m - 1) * pitch;
     } else {

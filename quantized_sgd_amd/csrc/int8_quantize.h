@@ -325,47 +325,61 @@ __global__ __launch_bounds__(256) void transpose_kernel(TransposeParams p) {
 }
 
 // Bytes of a row of levels in LDS: whole 64-byte steps, and 16 more so that rows
-// begin in different banks.
+// begin in different banks (never read).
 __host__ __device__ __forceinline__ uint32_t fused_pitch(uint32_t k) { return (k + 63) / 64 * 64 + 16; }
 
-// The levels of m rows of x into LDS and their scales into sx, by a workgroup of
-// eight waves; ends with a barrier. A row is taken by eight waves, or by fewer
-// where there are more rows. `part` holds 16 words.
+// Few rows of x quantized into LDS by a workgroup of eight waves: a row is taken by
+// eight waves, or by fewer where there are more rows, and is held in registers
+// between the maximum and the levels (kHeld chunks a thread).
+constexpr int kHeld = 4;
+__host__ __device__ __forceinline__ uint32_t waves_of_row(uint32_t m) { return m == 1 ? 8 : m == 2 ? 4 : m <= 4 ? 2 : 1; }
+// Whether that takes m rows of k.
+inline bool holds_rows(uint64_t m, uint64_t k) { return m <= 8 && k <= waves_of_row((uint32_t)m) * 512 * kHeld; }
+
 template <class X>
-__device__ __forceinline__ void quantize_to_lds(const X *x, uint64_t ldx, uint32_t m, uint32_t k, uint32_t pitch,
-                                                int8_t *levels, float *sx, uint32_t *part) {
-    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const uint32_t share = m == 1 ? 8 : m == 2 ? 4 : m <= 4 ? 2 : 1;  // waves of a row
-    const uint32_t at = wave % share * 512 + lane * 8, step = share * 512;
-    for (uint32_t r0 = 0; r0 < m; r0 += 8 / share) {
-        const uint32_t row = r0 + wave / share;
-        const X *from = x + (uint64_t)row * ldx;
-        uint32_t amax = 0;
-        if (row < m)
-            for (uint32_t c = at; c < k; c += step) {
-                float y[8];
-                Eight<X> raw;
-                fetch(from, c, k, raw);
-                settle(c, k, raw, y);
-                amax = largest(amax, y);
-            }
-        amax = wave_max(amax);
-        if (lane == 0) part[wave] = amax;
-        __syncthreads();
-        for (uint32_t i = 0; i < share; ++i) amax = max(amax, part[wave / share * share + i]);
-        const RowScale s = row_scale(amax);
-        if (row < m) {
-            if (at == 0) sx[row] = s.scale;
-            for (uint32_t c = at; c < pitch; c += step) {
-                float y[8];
-                Eight<X> raw;
-                fetch(from, c, k, raw);
-                settle(c, k, raw, y);
-                put_levels(levels + (uint64_t)row * pitch, c, pitch, y, s);
-            }
+struct HeldRow {
+    Eight<X> v[kHeld];
+    uint32_t row, at, step;  // the wave's row; the lane's first column and the next one's distance
+};
+template <class X>
+__device__ __forceinline__ void load_row(const X *x, uint64_t ldx, uint32_t m, uint32_t k, HeldRow<X> &h) {
+    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, share = waves_of_row(m);
+    h.row = wave / share;
+    h.at = wave % share * 512 + lane * 8;
+    h.step = share * 512;
+    const X *from = x + (uint64_t)min(h.row, m - 1) * ldx;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+        if (h.step * i < k) fetch(from, h.at + h.step * i, k, h.v[i]);
+}
+// The levels to LDS, the scales to sx; ends with a barrier. `part` holds 8 words.
+template <class X>
+__device__ __forceinline__ void quantize_to_lds(HeldRow<X> &h, uint32_t m, uint32_t k, uint32_t pitch, int8_t *levels,
+                                                float *sx, uint32_t *part) {
+    const uint32_t wave = threadIdx.x >> 6, share = waves_of_row(m);
+    float y[kHeld][8];
+    uint32_t amax = 0;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+        if (h.step * i < k) {
+            settle(h.at + h.step * i, k, h.v[i], y[i]);
+            amax = largest(amax, y[i]);
         }
-        __syncthreads();
+    amax = wave_max(amax);
+    if ((threadIdx.x & 63) == 0) part[wave] = amax;
+    __syncthreads();
+    for (uint32_t i = 0; i < share; ++i) amax = max(amax, part[wave / share * share + i]);
+    const RowScale s = row_scale(amax);
+    if (h.row < m) {
+        if (h.at == 0) sx[h.row] = s.scale;
+        int8_t *out = levels + (uint64_t)h.row * pitch;
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) {
+            const uint32_t c = h.at + h.step * i;
+            if (h.step * i < k && c < pitch) put_levels(out, c, pitch, y[i], s);
+        }
     }
+    __syncthreads();
 }
 
 // Copies rows of bytes to a row stride that is a multiple of 16, zeros past the

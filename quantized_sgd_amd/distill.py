@@ -10,7 +10,7 @@ import functools
 
 import torch
 
-from ._ops import DTYPE, FLOATS, check, function, matrix, on, raw_stream, same_device, scratch, u64, vector, vp
+from ._ops import DTYPE, FLOATS, check, function, matrix, on, raw_stream, scratch, u64, vector, vp
 
 __all__ = ["distill_topk", "distill_topk_backward", "distill_topk_step"]
 
@@ -28,7 +28,12 @@ _teacher_p = ctypes.POINTER(_Teacher)
 
 @functools.lru_cache(maxsize=1024)
 def _workspace_bytes(rows, vocab, dtype):
-    return function("qsgd_distill_workspace", u64, u64, u64, _int)(rows, vocab, DTYPE[dtype])
+    return function("qsgd_distill_workspace", u64, u64, u64, _int)(rows, vocab, dtype)
+
+
+@functools.lru_cache(maxsize=1)
+def _max_entries():
+    return function("qsgd_distill_max_entries", ctypes.c_uint32)()
 
 
 def _teacher(z, idx, t, tau, teacher_lse):
@@ -36,14 +41,12 @@ def _teacher(z, idx, t, tau, teacher_lse):
     entries' description."""
     ldz = matrix(z, "z", FLOATS)
     rows, dev = z.shape[0], z.device
-    ldi = matrix(idx, "idx", _INDEX, rows, None)
+    ldi = matrix(idx, "idx", _INDEX, rows, None, dev)
     k = idx.shape[1]
-    ldt = matrix(t, "t", FLOATS, rows, k)
-    same_device(dev, idx=idx, t=t)
+    ldt = matrix(t, "t", FLOATS, rows, k, dev)
     lse = vector(teacher_lse, "teacher_lse", rows, dev)
-    most = function("qsgd_distill_max_entries", ctypes.c_uint32)()
-    if k > most:
-        raise ValueError(f"at most {most} entries a row, got {k}")
+    if k > _max_entries():
+        raise ValueError(f"at most {_max_entries()} entries a row, got {k}")
     if not 1e-30 <= tau <= 1e30:
         raise ValueError(f"tau must be between 1e-30 and 1e30, got {tau}")
     return ldz, _Teacher(idx.data_ptr(), t.data_ptr(), DTYPE[idx.dtype], DTYPE[t.dtype], ldi, ldt, k, tau, lse)
@@ -51,9 +54,8 @@ def _teacher(z, idx, t, tau, teacher_lse):
 
 def _gradient_out(z, ldz, out):
     if out is None:
-        out = torch.empty(z.shape, dtype=z.dtype, device=z.device)
-    ld = matrix(out, "out", (z.dtype,), *z.shape)
-    same_device(z.device, out=out)
+        return torch.empty(z.shape, dtype=z.dtype, device=z.device), max(z.shape[1], 1)
+    ld = matrix(out, "out", (z.dtype,), *z.shape, z.device)
     if out.data_ptr() == z.data_ptr() and ld != ldz:
         raise ValueError("out in z's place must have z's row stride")
     return out, ld
@@ -72,8 +74,8 @@ def distill_topk(z: torch.Tensor, idx: torch.Tensor, t: torch.Tensor, tau: float
     dev = z.device
     with on(dev, stream):
         loss = torch.empty(rows, dtype=torch.float32, device=dev)
-        stats = torch.empty(rows, 4, dtype=torch.float32, device=dev)
-        ws = scratch(_workspace_bytes(rows, vocab, z.dtype), dev)
+        stats = torch.empty((rows, 4), dtype=torch.float32, device=dev)
+        ws = scratch(_workspace_bytes(rows, vocab, DTYPE[z.dtype]), dev)
         check(function("qsgd_distill_forward", _int, vp, _int, u64, u64, u64, _teacher_p, vp, vp, vp, vp)(
             z.data_ptr(), DTYPE[z.dtype], rows, vocab, ldz, te, loss.data_ptr(), stats.data_ptr(),
             None if ws is None else ws.data_ptr(), raw_stream(dev)), "qsgd_distill_forward")
@@ -88,8 +90,7 @@ def distill_topk_backward(z: torch.Tensor, idx: torch.Tensor, t: torch.Tensor, s
     ldz, te = _teacher(z, idx, t, tau, teacher_lse)
     rows, vocab = z.shape
     dev = z.device
-    matrix(stats, "stats", (torch.float32,), rows, 4)
-    same_device(dev, stats=stats)
+    matrix(stats, "stats", (torch.float32,), rows, 4, dev)
     if not stats.is_contiguous():
         raise ValueError("stats must be contiguous")
     g = vector(grad_loss, "grad_loss", rows, dev)
@@ -112,7 +113,7 @@ def distill_topk_step(z: torch.Tensor, idx: torch.Tensor, t: torch.Tensor, grad_
     with on(dev, stream):
         out, ld = _gradient_out(z, ldz, out)
         loss = torch.empty(rows, dtype=torch.float32, device=dev)
-        ws = scratch(_workspace_bytes(rows, vocab, z.dtype), dev)
+        ws = scratch(_workspace_bytes(rows, vocab, DTYPE[z.dtype]), dev)
         check(function("qsgd_distill_step", _int, vp, _int, u64, u64, u64, _teacher_p, vp, vp, vp, u64, vp, vp)(
             z.data_ptr(), DTYPE[z.dtype], rows, vocab, ldz, te, g, loss.data_ptr(), out.data_ptr(), ld,
             None if ws is None else ws.data_ptr(), raw_stream(dev)), "qsgd_distill_step")

@@ -11,7 +11,7 @@ import functools
 
 import torch
 
-from ._ops import DTYPE, FLOATS, check, function, matrix, on, raw_stream, same_device, scratch, u64, vector, vp
+from ._ops import DTYPE, FLOATS, check, function, matrix, on, raw_stream, scratch, u64, vector, vp
 
 __all__ = ["int8_quantize", "int8_matmul", "int8_linear", "int8_linear_backward"]
 
@@ -52,11 +52,11 @@ def int8_quantize(x: torch.Tensor, fold=None, transpose: bool = False, out=None,
     f = vector(fold, "fold", length, dev)
     with on(dev, stream):
         if out is None:
-            out = torch.empty(n, length, dtype=torch.int8, device=dev)
+            out, ldl = torch.empty((n, length), dtype=torch.int8, device=dev), max(length, 1)
+        else:
+            ldl = matrix(out, "out", _I8, n, length, dev)
         if scale is None:
             scale = torch.empty(n, dtype=torch.float32, device=dev)
-        ldl = matrix(out, "out", _I8, n, length)
-        same_device(dev, out=out)
         s = vector(scale, "scale", n, dev)
         if transpose:
             ws = scratch(_quantize_t_bytes(rows, cols), dev)
@@ -77,18 +77,19 @@ def int8_matmul(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb=None, bia
     int8 with any row stride; the sum over K is exact."""
     lda = matrix(a, "a", _I8)
     m, k = a.shape
-    ldb = matrix(b, "b", _I8, None, k)
-    n = b.shape[0]
     dev = a.device
-    same_device(dev, b=b)
+    ldb = matrix(b, "b", _I8, None, k, dev)
+    n = b.shape[0]
     if sa is None:
         raise ValueError("sa must be a tensor")
     pa, pb, pbias = vector(sa, "sa", m, dev), vector(sb, "sb", n, dev), vector(bias, "bias", n, dev)
     with on(dev, stream):
-        if out is None:
-            out = torch.empty(m, n, dtype=dtype, device=dev)
-        ldy = matrix(out, "out", FLOATS, m, n)
-        same_device(dev, out=out)
+        if out is None and dtype in FLOATS:
+            out, ldy = torch.empty((m, n), dtype=dtype, device=dev), max(n, 1)
+        elif out is None:
+            raise ValueError(f"dtype must be one of {', '.join(map(str, FLOATS))}, got {dtype}")
+        else:
+            ldy = matrix(out, "out", FLOATS, m, n, dev)
         ap, bp = a.data_ptr(), b.data_ptr()
         ws = scratch(_matmul_bytes(ap & 15, lda, bp & 15, ldb, m, n, k), dev)
         check(function("qsgd_int8_matmul", _int, vp, u64, vp, vp, u64, vp, vp, vp, _int, u64, u64, u64, u64, vp, vp)(
@@ -104,18 +105,17 @@ def int8_linear(x: torch.Tensor, w: torch.Tensor, sw: torch.Tensor, bias=None, k
     16) and sx their scales, which int8_linear_backward takes."""
     ldx = matrix(x, "x", FLOATS)
     m, k = x.shape
-    ldw = matrix(w, "w", _I8, None, k)
-    n = w.shape[0]
     dev = x.device
-    same_device(dev, w=w)
+    ldw = matrix(w, "w", _I8, None, k, dev)
+    n = w.shape[0]
     if sw is None:
         raise ValueError("sw must be a tensor")
     psw, pbias = vector(sw, "sw", n, dev), vector(bias, "bias", n, dev)
     with on(dev, stream):
         if out is None:
-            out = torch.empty(m, n, dtype=x.dtype, device=dev)
-        ldy = matrix(out, "out", (x.dtype,), m, n)
-        same_device(dev, out=out)
+            out, ldy = torch.empty((m, n), dtype=x.dtype, device=dev), max(n, 1)
+        else:
+            ldy = matrix(out, "out", (x.dtype,), m, n, dev)
         wp = w.data_ptr()
         xq = sx = None
         ldq = 0
@@ -140,11 +140,10 @@ def int8_linear_backward(gy: torch.Tensor, xq: torch.Tensor, sx: torch.Tensor, w
     gx, per column for gw). Returns (gx, gw), None for one not needed."""
     ldg = matrix(gy, "gy", FLOATS)
     m, n = gy.shape
-    ldq = matrix(xq, "xq", _I8, m, None)
-    k = xq.shape[1]
-    ldw = matrix(w, "w", _I8, n, k)
     dev = gy.device
-    same_device(dev, xq=xq, w=w)
+    ldq = matrix(xq, "xq", _I8, m, None, dev)
+    k = xq.shape[1]
+    ldw = matrix(w, "w", _I8, n, k, dev)
     if sx is None or sw is None:
         raise ValueError("sx and sw must be tensors")
     psx, psw = vector(sx, "sx", m, dev), vector(sw, "sw", n, dev)
