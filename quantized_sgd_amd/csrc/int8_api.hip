@@ -39,38 +39,57 @@ qsgd_status quantize_rows(const void *x, qsgd_dtype dtype, uint64_t rows, uint64
     });
 }
 
-// Runs of rows for the column maxima: enough workgroups for the chip, at least 32
-// rows each.
+// Runs of rows for the column maxima, of at least 32 rows: few enough to be joined
+// where they are used for up to 2048 rows (it saves a launch), else enough
+// workgroups for the chip.
 uint32_t column_splits(uint64_t rows, uint64_t cols) {
     const uint64_t blocks = std::max<uint64_t>(1, div_up(cols, 512));
-    return (uint32_t)std::max<uint64_t>(1, std::min({(uint64_t)kMaxSplits, div_up(1024, blocks), div_up(rows, 32)}));
+    const uint64_t most = rows <= 2048 ? kFewSplits : std::min<uint64_t>(kMaxSplits, div_up(1024, blocks));
+    return (uint32_t)std::max<uint64_t>(1, std::min(most, div_up(rows, 32)));
+}
+
+TransposeParams transpose_params(const void *x, uint64_t rows, uint64_t cols, uint64_t ldx, const float *fold,
+                                 int8_t *levels, uint64_t ldl, float *scale, uint64_t wide, void *part, uint32_t splits) {
+    return {x, fold, levels, scale, (uint32_t *)part, ldx, ldl, (uint32_t)rows, (uint32_t)cols, (uint32_t)wide, splits,
+            (uint32_t)div_up(rows, splits), (uint32_t)std::max<uint64_t>(1, div_up(wide, 128)), (uint32_t)div_up(cols, 64)};
+}
+
+uint64_t max_blocks(const TransposeParams &p) { return div_up(p.cols, 512) * p.splits; }
+uint64_t tile_blocks(const TransposeParams &p) { return (uint64_t)p.row_tiles * p.col_tiles; }
+
+// The levels of the columns whose maxima are in p.part.
+template <class T>
+void launch_transpose(const TransposeParams &p, hipStream_t stream) {
+    if (p.splits > kFewSplits || p.rows == 0) column_scale_kernel<<<(uint32_t)div_up(p.cols, 64), 1024, 0, stream>>>(p);
+    if (p.rows) transpose_kernel<T><<<grid_of(tile_blocks(p)), 256, 0, stream>>>(p);
 }
 
 qsgd_status quantize_columns(const void *x, qsgd_dtype dtype, uint64_t rows, uint64_t cols, uint64_t ldx,
                              const float *fold, int8_t *levels, uint64_t ldl, float *scale, uint64_t wide,
                              void *workspace, hipStream_t stream) {
     if (cols == 0) return QSGD_OK;
-    const uint32_t splits = column_splits(rows, cols);
-    const uint32_t tr = (uint32_t)std::max<uint64_t>(1, div_up(wide, 128)), tc = (uint32_t)div_up(cols, 64);
+    const TransposeParams p =
+        transpose_params(x, rows, cols, ldx, fold, levels, ldl, scale, wide, workspace, column_splits(rows, cols));
     return with_type(dtype, [&](auto t) {
         using T = decltype(t);
-        const TransposeParams p{x, fold, levels, scale, (uint32_t *)workspace, ldx, ldl, (uint32_t)rows, (uint32_t)cols,
-                                (uint32_t)wide, splits, (uint32_t)div_up(rows, splits), tr, tc};
-        column_max_kernel<T><<<dim3((uint32_t)div_up(cols, 512), splits), 256, 0, stream>>>(p);
-        column_scale_kernel<<<(uint32_t)div_up(cols, 64), 1024, 0, stream>>>(p);
-        if (rows) transpose_kernel<T><<<grid_of((uint64_t)tr * tc), 256, 0, stream>>>(p);
+        column_max_kernel<T><<<(uint32_t)max_blocks(p), 256, 0, stream>>>(p);
+        launch_transpose<T>(p, stream);
         return launched();
     });
 }
 
-qsgd_status transpose_bytes(const int8_t *x, uint64_t rows, uint64_t cols, uint64_t ldx, int8_t *out, uint64_t ldo,
-                            uint64_t wide, hipStream_t stream) {
-    if (cols == 0 || wide == 0) return QSGD_OK;
-    const uint32_t tr = (uint32_t)div_up(wide, 128), tc = (uint32_t)div_up(cols, 64);
-    const TransposeParams p{x, nullptr, out, nullptr, nullptr, ldx, ldo, (uint32_t)rows, (uint32_t)cols, (uint32_t)wide,
-                            0, 0, tr, tc};
-    transpose_kernel<int8_t><<<grid_of((uint64_t)tr * tc), 256, 0, stream>>>(p);
-    return launched();
+// Everything before the gradient's products but the columns' levels.
+template <class T>
+void launch_gradient_inputs(const GradientParams &p, hipStream_t stream) {
+    const uint64_t blocks = p.n_max + p.n_rows + p.n_w + p.n_x;
+    if (blocks == 0) return;
+    const uint32_t n = p.rows.wide;
+    const dim3 grid = grid_of(blocks);
+    if (n <= 1024) gradient_inputs_kernel<T, 64, 2><<<grid, 256, 0, stream>>>(p);
+    else if (n <= 2048) gradient_inputs_kernel<T, 256, 1><<<grid, 256, 0, stream>>>(p);
+    else if (n <= 4096) gradient_inputs_kernel<T, 256, 2><<<grid, 256, 0, stream>>>(p);
+    else if (n <= 8192) gradient_inputs_kernel<T, 256, 4><<<grid, 256, 0, stream>>>(p);
+    else gradient_inputs_kernel<T, 256, 0><<<grid, 256, 0, stream>>>(p);
 }
 
 // ---- product ----
@@ -360,19 +379,27 @@ qsgd_status qsgd_int8_linear_backward(const void *gy, qsgd_dtype dtype, uint64_t
     char *ws = (char *)workspace;
     int8_t *gq = (int8_t *)(ws + b.gq), *wt = (int8_t *)(ws + b.wt), *hq = (int8_t *)(ws + b.hq), *xt = (int8_t *)(ws + b.xt);
     float *sg = (float *)(ws + b.sg), *sh = (float *)(ws + b.sh);
-    qsgd_status st = QSGD_OK;
-    if (st == QSGD_OK && gx) {
-        st = quantize_rows(gy, dtype, m, n, ldgy, sw, gq, b.ldn, sg, b.ldn, stream);
-        if (st == QSGD_OK) st = transpose_bytes(w, n, k, ldw, wt, b.ldn, b.ldn, stream);
-        if (st == QSGD_OK)
-            st = run_matmul(b.gx, gq, sg, wt, nullptr, nullptr, gx, dtype, ldgx, b.ldn, b.ldn, m, k, n, ws + b.own, stream);
-    }
-    if (st == QSGD_OK && gw) {
-        st = quantize_columns(gy, dtype, m, n, ldgy, sx, hq, b.ldm, sh, b.ldm, ws + b.cols, stream);
-        if (st == QSGD_OK) st = transpose_bytes(xq, m, k, ldxq, xt, b.ldm, b.ldm, stream);
-        if (st == QSGD_OK)
-            st = run_matmul(b.gw, hq, sh, xt, nullptr, nullptr, gw, QSGD_F32, ldgw, b.ldm, b.ldm, n, k, m, ws + b.own, stream);
-    }
+    // A transposed matrix' rows are 0 past their end up to a multiple of 16.
+    GradientParams p{};
+    p.rows = {gy, sw, gq, sg, ldgy, b.ldn, (uint32_t)m, (uint32_t)n, (uint32_t)b.ldn};
+    p.w = transpose_params(w, n, k, ldw, nullptr, wt, b.ldn, nullptr, b.ldn, nullptr, 1);
+    p.columns = transpose_params(gy, m, n, ldgy, sx, hq, b.ldm, sh, b.ldm, ws + b.cols, column_splits(m, n));
+    p.x = transpose_params(xq, m, k, ldxq, nullptr, xt, b.ldm, nullptr, b.ldm, nullptr, 1);
+    const bool rows = gx && m, columns = gw && n;
+    p.n_rows = rows ? div_up(m, b.ldn <= 1024 ? 4 : 1) : 0;
+    p.n_w = rows && n ? tile_blocks(p.w) : 0;
+    p.n_max = columns ? max_blocks(p.columns) : 0;
+    p.n_x = columns && m ? tile_blocks(p.x) : 0;
+    qsgd_status st = with_type(dtype, [&](auto t) {
+        using T = decltype(t);
+        launch_gradient_inputs<T>(p, stream);
+        if (columns) launch_transpose<T>(p.columns, stream);
+        return launched();
+    });
+    if (st == QSGD_OK && gx)
+        st = run_matmul(b.gx, gq, sg, wt, nullptr, nullptr, gx, dtype, ldgx, b.ldn, b.ldn, m, k, n, ws + b.own, stream);
+    if (st == QSGD_OK && gw)
+        st = run_matmul(b.gw, hq, sh, xt, nullptr, nullptr, gw, QSGD_F32, ldgw, b.ldm, b.ldm, n, k, m, ws + b.own, stream);
     return st;
 }
 

@@ -95,9 +95,8 @@ __device__ __forceinline__ uint32_t largest(uint32_t amax, const float (&y)[8]) 
 // TPR threads take a row (a wave or the workgroup), each NV chunks of 8 values
 // that stay in registers; NV = 0 takes rows of any length, reading them twice.
 template <class T, int TPR, int NV>
-__global__ __launch_bounds__(256) void quantize_rows_kernel(QuantizeParams p) {
-    __shared__ uint32_t part[4];
-    const uint32_t row = (uint32_t)block_index() * (256 / TPR) + threadIdx.x / TPR;
+__device__ __forceinline__ void quantize_rows_block(const QuantizeParams &p, uint64_t block, uint32_t *part) {
+    const uint32_t row = (uint32_t)block * (256 / TPR) + threadIdx.x / TPR;
     const uint32_t t = threadIdx.x % TPR;
     if (row >= p.rows) return;  // a whole wave, or the workgroup
     const T *x = (const T *)p.x + (uint64_t)row * p.ldx;
@@ -164,6 +163,12 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(QuantizeParams p) {
     }
 }
 
+template <class T, int TPR, int NV>
+__global__ __launch_bounds__(256) void quantize_rows_kernel(QuantizeParams p) {
+    __shared__ uint32_t part[4];
+    quantize_rows_block<T, TPR, NV>(p, block_index(), part);
+}
+
 struct TransposeParams {
     const void *x;
     const float *fold;
@@ -178,14 +183,15 @@ struct TransposeParams {
 };
 
 constexpr uint32_t kMaxSplits = 256;
+constexpr uint32_t kFewSplits = 16;  // joined by the kernel that uses them
 
 // Column maxima of a run of rows: a wave takes every fourth row, a lane 8 columns.
 template <class T>
-__global__ __launch_bounds__(256) void column_max_kernel(TransposeParams p) {
-    __shared__ uint32_t part[3][512];
+__device__ __forceinline__ void column_max_block(const TransposeParams &p, uint32_t block, uint32_t (*part)[512]) {
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const uint32_t c = blockIdx.x * 512 + lane * 8;
-    const uint32_t lo = blockIdx.y * p.rows_per_split, hi = min(p.rows, lo + p.rows_per_split);
+    const uint32_t wide = (p.cols + 511) / 512, split = block / wide;
+    const uint32_t c = block % wide * 512 + lane * 8;
+    const uint32_t lo = split * p.rows_per_split, hi = min(p.rows, lo + p.rows_per_split);
     uint32_t amax[8] = {};
     if (c < p.cols) {
         const T *x = (const T *)p.x;
@@ -217,13 +223,18 @@ __global__ __launch_bounds__(256) void column_max_kernel(TransposeParams p) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const uint32_t m = max(max(amax[i], part[0][i * 64 + lane]), max(part[1][i * 64 + lane], part[2][i * 64 + lane]));
-            if (c + i < p.cols) p.part[(uint64_t)blockIdx.y * p.cols + c + i] = m;
+            if (c + i < p.cols) p.part[(uint64_t)split * p.cols + c + i] = m;
         }
     }
 }
+template <class T>
+__global__ __launch_bounds__(256) void column_max_kernel(TransposeParams p) {
+    __shared__ uint32_t part[3][512];
+    column_max_block<T>(p, blockIdx.x, part);
+}
 
-// Joins the runs' column maxima: a column's scale. 64 columns a workgroup, sixteen
-// threads a column.
+// Joins the runs' column maxima where there are more than kFewSplits: a column's
+// scale. 64 columns a workgroup, sixteen threads a column.
 static __global__ __launch_bounds__(1024) void column_scale_kernel(TransposeParams p) {
     __shared__ uint32_t part[16][64];
     const uint32_t c = blockIdx.x * 64 + (threadIdx.x & 63), g = threadIdx.x >> 6;
@@ -246,12 +257,9 @@ static __global__ __launch_bounds__(1024) void column_scale_kernel(TransposePara
 // columns have 33 words, which spreads a wave's writes over all banks. T = int8_t
 // moves bytes as they are.
 template <class T>
-__global__ __launch_bounds__(256) void transpose_kernel(TransposeParams p) {
+__device__ __forceinline__ void transpose_block(const TransposeParams &p, uint64_t block, uint32_t *tile, float2 *scales) {
     constexpr bool kBytes = sizeof(T) == 1;
-    __shared__ uint32_t tile[64 * 33];
-    __shared__ float2 scales[64];  // with its inverse
     const uint32_t t = threadIdx.x;
-    const uint64_t block = block_index();
     if (block >= (uint64_t)p.row_tiles * p.col_tiles) return;
     const uint32_t r0 = (uint32_t)(block % p.row_tiles) * 128, c0 = (uint32_t)(block / p.row_tiles) * 64;
     const uint32_t c = c0 + (t & 7) * 8, r = r0 + (t >> 3) * 4;
@@ -288,7 +296,22 @@ __global__ __launch_bounds__(256) void transpose_kernel(TransposeParams p) {
             tile[((t & 7) * 8 + i) * 33 + (t >> 3)] =
                 (uint32_t)b[0][i] | (uint32_t)b[1][i] << 8 | (uint32_t)b[2][i] << 16 | (uint32_t)b[3][i] << 24;
     } else {
-        if (t < 64) {
+        if (p.splits <= kFewSplits) {  // this tile's columns' scales, joined here
+            const uint32_t col = c0 + (t & 63);
+            uint32_t m = 0;
+            if (col < p.cols) {
+#pragma unroll
+                for (uint32_t s = 0; s < kFewSplits; s += 4)
+                    if (s + (t >> 6) < p.splits) m = max(m, p.part[(uint64_t)(s + (t >> 6)) * p.cols + col]);
+            }
+            tile[t] = m;
+            __syncthreads();
+            if (t < 64) {
+                const RowScale s = row_scale(max(max(tile[t], tile[64 + t]), max(tile[128 + t], tile[192 + t])));
+                scales[t] = make_float2(s.scale, s.inv);
+                if (r0 == 0 && col < p.cols) p.scale[col] = s.scale;
+            }
+        } else if (t < 64) {
             const float s = c0 + t < p.cols ? p.scale[c0 + t] : 0.0f;
             scales[t] = make_float2(s, 1.0f / s);
         }
@@ -322,6 +345,33 @@ __global__ __launch_bounds__(256) void transpose_kernel(TransposeParams p) {
                 if (rr + i < p.wide) out[i] = (int8_t)(w[i / 4] >> (8 * (i % 4)));
         }
     }
+}
+
+template <class T>
+__global__ __launch_bounds__(256) void transpose_kernel(TransposeParams p) {
+    __shared__ uint32_t tile[64 * 33];
+    __shared__ float2 scales[64];  // with its inverse
+    transpose_block<T>(p, block_index(), tile, scales);
+}
+
+// What the gradient's products need, in one launch of workgroups of four kinds: the
+// column maxima of gy, its rows' levels, w and xq transposed.
+struct GradientParams {
+    QuantizeParams rows;
+    TransposeParams columns, w, x;
+    uint64_t n_max, n_rows, n_w, n_x;  // workgroups of each
+};
+template <class T, int TPR, int NV>
+__global__ __launch_bounds__(256) void gradient_inputs_kernel(GradientParams p) {
+    __shared__ uint32_t lds[64 * 33];
+    uint64_t block = block_index();
+    if (block < p.n_max) return column_max_block<T>(p.columns, (uint32_t)block, (uint32_t(*)[512])lds);
+    block -= p.n_max;
+    if (block < p.n_rows) return quantize_rows_block<T, TPR, NV>(p.rows, block, lds);
+    block -= p.n_rows;
+    if (block < p.n_w) return transpose_block<int8_t>(p.w, block, lds, nullptr);
+    block -= p.n_w;
+    if (block < p.n_x) transpose_block<int8_t>(p.x, block, lds, nullptr);
 }
 
 // Bytes of a row of levels in LDS: whole 64-byte steps, and 16 more so that rows
@@ -391,9 +441,9 @@ struct RepackParams {
     uint32_t rows, cols;
 };
 
-static __global__ __launch_bounds__(256) void repack_kernel(RepackParams p) {
+__device__ __forceinline__ void repack_block(const RepackParams &p, uint64_t block) {
     const uint64_t per_row = p.ldd / 16;
-    const uint64_t at = block_index() * 256 + threadIdx.x;
+    const uint64_t at = block * 256 + threadIdx.x;
     if (at >= per_row * p.rows) return;
     const uint64_t row = at / per_row, c = at % per_row * 16;
     const int8_t *s = p.src + row * p.lds + c;
@@ -406,6 +456,8 @@ static __global__ __launch_bounds__(256) void repack_kernel(RepackParams p) {
     }
     *(uint4 *)(p.dst + row * p.ldd + c) = make_uint4(w[0], w[1], w[2], w[3]);
 }
+
+static __global__ __launch_bounds__(256) void repack_kernel(RepackParams p) { repack_block(p, block_index()); }
 
 }  // namespace ops
 }  // namespace qsgd
