@@ -60,7 +60,7 @@ uint64_t tile_blocks(const TransposeParams &p) { return (uint64_t)p.row_tiles * 
 // The levels of the columns whose maxima are in p.part.
 template <class T>
 void launch_transpose(const TransposeParams &p, hipStream_t stream) {
-    if (p.splits > kFewSplits || p.rows == 0) column_scale_kernel<<<(uint32_t)div_up(p.cols, 64), 1024, 0, stream>>>(p);
+    if (p.splits > kFewSplits || p.rows == 0) column_scale_kernel<<<grid_of(div_up(p.cols, 64)), 1024, 0, stream>>>(p);
     if (p.rows) transpose_kernel<T><<<grid_of(tile_blocks(p)), 256, 0, stream>>>(p);
 }
 

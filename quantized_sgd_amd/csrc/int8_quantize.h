@@ -237,7 +237,9 @@ __global__ __launch_bounds__(256) void column_max_kernel(TransposeParams p) {
 // scale. 64 columns a workgroup, sixteen threads a column.
 static __global__ __launch_bounds__(1024) void column_scale_kernel(TransposeParams p) {
     __shared__ uint32_t part[16][64];
-    const uint32_t c = blockIdx.x * 64 + (threadIdx.x & 63), g = threadIdx.x >> 6;
+    const uint64_t block = block_index();
+    if (block * 64 >= p.cols) return;
+    const uint32_t c = (uint32_t)block * 64 + (threadIdx.x & 63), g = threadIdx.x >> 6;
     uint32_t m = 0;
     if (c < p.cols) {
 #pragma unroll 8
