@@ -15,17 +15,11 @@ FLOATS = (torch.float32, torch.float16, torch.bfloat16)
 u64 = ctypes.c_uint64
 vp = ctypes.c_void_p
 
-_bound = {}
-
-
-def function(name: str, restype, *argtypes):
-    """The library's function with its C types, looked up once."""
-    f = _bound.get(name)
-    if f is None:
-        f = getattr(lib(), name)
-        f.argtypes = argtypes
-        f.restype = restype
-        _bound[name] = f
+def bind(name: str, restype, *argtypes):
+    """The library's function with its C types."""
+    f = getattr(lib(), name)
+    f.argtypes = argtypes
+    f.restype = restype
     return f
 
 
@@ -85,13 +79,17 @@ def on(device, stream):
     it)."""
     if stream is not None:
         return torch.cuda.stream(stream)
-    if device.index == torch.cuda.current_device():
+    if device.index == current_device():
         return _nothing
     return torch.cuda.device(device)
 
 
+current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def raw_stream(device) -> int:
-    return torch._C._cuda_getCurrentRawStream(device.index)
+    return _raw_stream(device.index)
 
 
 def scratch(nbytes: int, device):

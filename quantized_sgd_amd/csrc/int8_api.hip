@@ -180,6 +180,7 @@ void launch_tiles(const MatmulParams &p, hipStream_t stream) {
     // a tile that fills a CU: one workgroup a CU goes from tile to tile
     const bool stay = C::kLds > 80 * 1024 && tiles > kCus && p.steps_per_split >= C::S && p.splits == 1;
     q.stride = stay ? kCus / 8 : tiles;
+    q.band = p.tiles_m <= 6 ? p.tiles_m : 4;
     matmul_kernel<C, OUT><<<dim3(stay ? (uint32_t)kCus : tiles, p.splits), C::NW * 64, 0, stream>>>(q);
 }
 

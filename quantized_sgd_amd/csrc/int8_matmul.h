@@ -25,6 +25,7 @@ struct MatmulParams {
     uint32_t m, n, k;
     uint32_t tiles_m, tiles_n;
     uint32_t splits, steps_per_split;  // 128-byte steps of k
+    uint32_t band;    // tile rows that are gone through together, a column of them at a time
     uint32_t stride;  // tiles of an XCD's run that a workgroup goes on by: it takes every stride-th
 };
 
@@ -126,7 +127,7 @@ __global__ __launch_bounds__(C::NW * 64, 1) void matmul_kernel(MatmulParams p) {
     const uint32_t wm = wave / C::WN, wn = wave % C::WN;
 
     // Workgroups go round the 8 XCDs in turn; each XCD takes a contiguous run of
-    // tiles, in bands of 4 tile rows, so that the tiles an XCD works on together
+    // tiles, in bands of tile rows, so that the tiles an XCD works on together
     // share their rows of a and b in its L2 (8192^3: bands of 4 422 us, 2 431, 6 428, 8 436).
     const uint32_t tiles = p.tiles_m * p.tiles_n;
     const uint32_t xcd = blockIdx.x % 8;
@@ -146,9 +147,9 @@ __global__ __launch_bounds__(C::NW * 64, 1) void matmul_kernel(MatmulParams p) {
     const int8_t *a, *b;
     uint32_t oa[C::LA], ob[C::LB];
     const auto place = [&](uint32_t id, uint32_t set) __attribute__((always_inline)) {
-        const uint32_t band = id / (4 * p.tiles_n), in_band = id % (4 * p.tiles_n);
-        const uint32_t band_rows = min(4u, p.tiles_m - band * 4);
-        load_m = (band * 4 + in_band % band_rows) * C::BM;
+        const uint32_t band = id / (p.band * p.tiles_n), in_band = id % (p.band * p.tiles_n);
+        const uint32_t band_rows = min(p.band, p.tiles_m - band * p.band);
+        load_m = (band * p.band + in_band % band_rows) * C::BM;
         load_n = in_band / band_rows * C::BN;
         a = p.a + (uint64_t)load_m * p.lda + (uint64_t)k0 * 128;
         b = p.b + (uint64_t)load_n * p.ldb + (uint64_t)k0 * 128;

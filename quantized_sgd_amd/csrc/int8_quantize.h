@@ -183,7 +183,7 @@ struct TransposeParams {
 };
 
 constexpr uint32_t kMaxSplits = 256;
-constexpr uint32_t kFewSplits = 16;  // joined by the kernel that uses them
+constexpr uint32_t kFewSplits = 32;  // joined by the kernel that uses them
 
 // Column maxima of a run of rows: a wave takes every fourth row, a lane 8 columns.
 template <class T>

@@ -10,7 +10,7 @@ import functools
 
 import torch
 
-from ._ops import DTYPE, FLOATS, check, function, matrix, on, raw_stream, scratch, u64, vector, vp
+from ._ops import DTYPE, FLOATS, bind, check, matrix, on, raw_stream, scratch, u64, vector, vp
 
 __all__ = ["distill_topk", "distill_topk_backward", "distill_topk_step"]
 
@@ -26,14 +26,31 @@ class _Teacher(ctypes.Structure):
 _teacher_p = ctypes.POINTER(_Teacher)
 
 
+_TYPES = {
+    "qsgd_distill_workspace": (u64, u64, u64, _int),
+    "qsgd_distill_max_entries": (ctypes.c_uint32,),
+    "qsgd_distill_forward": (_int, vp, _int, u64, u64, u64, _teacher_p, vp, vp, vp, vp),
+    "qsgd_distill_backward": (_int, vp, _int, u64, u64, u64, _teacher_p, vp, vp, vp, u64, vp),
+    "qsgd_distill_step": (_int, vp, _int, u64, u64, u64, _teacher_p, vp, vp, vp, u64, vp, vp),
+}
+_bound = {}
+
+
+def _c(name):
+    f = _bound.get(name)
+    if f is None:
+        f = _bound[name] = bind(name, *_TYPES[name])
+    return f
+
+
 @functools.lru_cache(maxsize=1024)
 def _workspace_bytes(rows, vocab, dtype):
-    return function("qsgd_distill_workspace", u64, u64, u64, _int)(rows, vocab, dtype)
+    return _c("qsgd_distill_workspace")(rows, vocab, dtype)
 
 
 @functools.lru_cache(maxsize=1)
 def _max_entries():
-    return function("qsgd_distill_max_entries", ctypes.c_uint32)()
+    return _c("qsgd_distill_max_entries")()
 
 
 def _teacher(z, idx, t, tau, teacher_lse):
@@ -76,7 +93,7 @@ def distill_topk(z: torch.Tensor, idx: torch.Tensor, t: torch.Tensor, tau: float
         loss = torch.empty(rows, dtype=torch.float32, device=dev)
         stats = torch.empty((rows, 4), dtype=torch.float32, device=dev)
         ws = scratch(_workspace_bytes(rows, vocab, DTYPE[z.dtype]), dev)
-        check(function("qsgd_distill_forward", _int, vp, _int, u64, u64, u64, _teacher_p, vp, vp, vp, vp)(
+        check(_c("qsgd_distill_forward")(
             z.data_ptr(), DTYPE[z.dtype], rows, vocab, ldz, te, loss.data_ptr(), stats.data_ptr(),
             None if ws is None else ws.data_ptr(), raw_stream(dev)), "qsgd_distill_forward")
     return loss, stats
@@ -96,7 +113,7 @@ def distill_topk_backward(z: torch.Tensor, idx: torch.Tensor, t: torch.Tensor, s
     g = vector(grad_loss, "grad_loss", rows, dev)
     with on(dev, stream):
         out, ld = _gradient_out(z, ldz, out)
-        check(function("qsgd_distill_backward", _int, vp, _int, u64, u64, u64, _teacher_p, vp, vp, vp, u64, vp)(
+        check(_c("qsgd_distill_backward")(
             z.data_ptr(), DTYPE[z.dtype], rows, vocab, ldz, te, stats.data_ptr(), g, out.data_ptr(), ld,
             raw_stream(dev)), "qsgd_distill_backward")
     return out
@@ -114,7 +131,7 @@ def distill_topk_step(z: torch.Tensor, idx: torch.Tensor, t: torch.Tensor, grad_
         out, ld = _gradient_out(z, ldz, out)
         loss = torch.empty(rows, dtype=torch.float32, device=dev)
         ws = scratch(_workspace_bytes(rows, vocab, DTYPE[z.dtype]), dev)
-        check(function("qsgd_distill_step", _int, vp, _int, u64, u64, u64, _teacher_p, vp, vp, vp, u64, vp, vp)(
+        check(_c("qsgd_distill_step")(
             z.data_ptr(), DTYPE[z.dtype], rows, vocab, ldz, te, g, loss.data_ptr(), out.data_ptr(), ld,
             None if ws is None else ws.data_ptr(), raw_stream(dev)), "qsgd_distill_step")
     return loss, out

@@ -11,7 +11,7 @@ import functools
 
 import torch
 
-from ._ops import DTYPE, FLOATS, check, function, matrix, on, raw_stream, scratch, u64, vector, vp
+from ._ops import DTYPE, FLOATS, bind, check, matrix, on, raw_stream, scratch, u64, vector, vp
 
 __all__ = ["int8_quantize", "int8_matmul", "int8_linear", "int8_linear_backward"]
 
@@ -19,25 +19,46 @@ _int = ctypes.c_int
 _I8 = (torch.int8,)
 
 
+_TYPES = {
+    "qsgd_int8_quantize_transposed_workspace": (u64, u64, u64),
+    "qsgd_int8_matmul_workspace": (u64, vp, u64, vp, u64, u64, u64, u64),
+    "qsgd_int8_linear_workspace": (u64, vp, u64, u64, u64, u64, _int),
+    "qsgd_int8_linear_backward_workspace": (u64, u64, u64, u64),
+    "qsgd_int8_quantize_transposed": (_int, vp, _int, u64, u64, u64, vp, vp, u64, vp, vp, vp),
+    "qsgd_int8_quantize": (_int, vp, _int, u64, u64, u64, vp, vp, u64, vp, vp),
+    "qsgd_int8_matmul": (_int, vp, u64, vp, vp, u64, vp, vp, vp, _int, u64, u64, u64, u64, vp, vp),
+    "qsgd_int8_linear": (_int, vp, _int, u64, vp, u64, vp, vp, vp, u64, vp, u64, vp, u64, u64, u64, vp, vp),
+    "qsgd_int8_linear_backward": (_int, vp, _int, u64, vp, u64, vp, vp, u64, vp, vp, u64, vp, u64, u64, u64, u64, vp, vp),
+}
+_bound = {}
+
+
+def _c(name):
+    f = _bound.get(name)
+    if f is None:
+        f = _bound[name] = bind(name, *_TYPES[name])
+    return f
+
+
 @functools.lru_cache(maxsize=1024)
 def _quantize_t_bytes(rows, cols):
-    return function("qsgd_int8_quantize_transposed_workspace", u64, u64, u64)(rows, cols)
+    return _c("qsgd_int8_quantize_transposed_workspace")(rows, cols)
 
 
 @functools.lru_cache(maxsize=1024)
 def _matmul_bytes(a_off, lda, b_off, ldb, m, n, k):
-    return function("qsgd_int8_matmul_workspace", u64, vp, u64, vp, u64, u64, u64, u64)(
+    return _c("qsgd_int8_matmul_workspace")(
         16 + a_off, lda, 16 + b_off, ldb, m, n, k)
 
 
 @functools.lru_cache(maxsize=1024)
 def _linear_bytes(w_off, ldw, m, n, k, keep):
-    return function("qsgd_int8_linear_workspace", u64, vp, u64, u64, u64, u64, _int)(16 + w_off, ldw, m, n, k, keep)
+    return _c("qsgd_int8_linear_workspace")(16 + w_off, ldw, m, n, k, keep)
 
 
 @functools.lru_cache(maxsize=1024)
 def _backward_bytes(m, n, k):
-    return function("qsgd_int8_linear_backward_workspace", u64, u64, u64, u64)(m, n, k)
+    return _c("qsgd_int8_linear_backward_workspace")(m, n, k)
 
 
 def int8_quantize(x: torch.Tensor, fold=None, transpose: bool = False, out=None, scale=None, stream=None):
@@ -60,11 +81,11 @@ def int8_quantize(x: torch.Tensor, fold=None, transpose: bool = False, out=None,
         s = vector(scale, "scale", n, dev)
         if transpose:
             ws = scratch(_quantize_t_bytes(rows, cols), dev)
-            check(function("qsgd_int8_quantize_transposed", _int, vp, _int, u64, u64, u64, vp, vp, u64, vp, vp, vp)(
+            check(_c("qsgd_int8_quantize_transposed")(
                 x.data_ptr(), DTYPE[x.dtype], rows, cols, ldx, f, out.data_ptr(), max(ldl, length), s,
                 None if ws is None else ws.data_ptr(), raw_stream(dev)), "qsgd_int8_quantize_transposed")
         else:
-            check(function("qsgd_int8_quantize", _int, vp, _int, u64, u64, u64, vp, vp, u64, vp, vp)(
+            check(_c("qsgd_int8_quantize")(
                 x.data_ptr(), DTYPE[x.dtype], rows, cols, ldx, f, out.data_ptr(), ldl, s, raw_stream(dev)),
                 "qsgd_int8_quantize")
     return out, scale
@@ -92,7 +113,7 @@ def int8_matmul(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb=None, bia
             ldy = matrix(out, "out", FLOATS, m, n, dev)
         ap, bp = a.data_ptr(), b.data_ptr()
         ws = scratch(_matmul_bytes(ap & 15, lda, bp & 15, ldb, m, n, k), dev)
-        check(function("qsgd_int8_matmul", _int, vp, u64, vp, vp, u64, vp, vp, vp, _int, u64, u64, u64, u64, vp, vp)(
+        check(_c("qsgd_int8_matmul")(
             ap, lda, pa, bp, ldb, pb, pbias, out.data_ptr(), DTYPE[out.dtype], ldy, m, n, k,
             None if ws is None else ws.data_ptr(), raw_stream(dev)), "qsgd_int8_matmul")
     return out
@@ -124,8 +145,7 @@ def int8_linear(x: torch.Tensor, w: torch.Tensor, sw: torch.Tensor, bias=None, k
             xq = torch.empty(m, ldq, dtype=torch.int8, device=dev)
             sx = torch.empty(m, dtype=torch.float32, device=dev)
         ws = scratch(_linear_bytes(wp & 15, ldw, m, n, k, int(keep)), dev)
-        check(function("qsgd_int8_linear", _int, vp, _int, u64, vp, u64, vp, vp, vp, u64, vp, u64, vp, u64, u64, u64, vp,
-                       vp)(
+        check(_c("qsgd_int8_linear")(
             x.data_ptr(), DTYPE[x.dtype], ldx, wp, ldw, psw, pbias, out.data_ptr(), ldy,
             xq.data_ptr() if keep else None, ldq, sx.data_ptr() if keep else None, m, n, k,
             None if ws is None else ws.data_ptr(), raw_stream(dev)), "qsgd_int8_linear")
@@ -151,8 +171,7 @@ def int8_linear_backward(gy: torch.Tensor, xq: torch.Tensor, sx: torch.Tensor, w
         gx = torch.empty(m, k, dtype=gy.dtype, device=dev) if need_gx else None
         gw = torch.empty(n, k, dtype=torch.float32, device=dev) if need_gw else None
         ws = scratch(_backward_bytes(m, n, k), dev)
-        check(function("qsgd_int8_linear_backward", _int, vp, _int, u64, vp, u64, vp, vp, u64, vp, vp, u64, vp, u64, u64,
-                       u64, u64, vp, vp)(
+        check(_c("qsgd_int8_linear_backward")(
             gy.data_ptr(), DTYPE[gy.dtype], ldg, xq.data_ptr(), ldq, psx, w.data_ptr(), ldw, psw,
             gx.data_ptr() if need_gx else None, max(k, 1), gw.data_ptr() if need_gw else None, max(k, 1), m, n, k,
             None if ws is None else ws.data_ptr(), raw_stream(dev)), "qsgd_int8_linear_backward")

@@ -23,7 +23,7 @@ def test_every_declared_function_is_exported():
 
 def test_int8_argument_checks():
     from quantized_sgd_amd import int8  # noqa: F401 (its C types are set on use)
-    from quantized_sgd_amd._ops import function, u64, vp
+    from quantized_sgd_amd._ops import bind as function, u64, vp
     import ctypes
     i = ctypes.c_int
     quant = function("qsgd_int8_quantize", i, vp, i, u64, u64, u64, vp, vp, u64, vp, vp)
@@ -69,7 +69,7 @@ def test_int8_argument_checks():
 
 
 def test_workspaces_of_empty_sizes():
-    from quantized_sgd_amd._ops import function, u64, vp
+    from quantized_sgd_amd._ops import bind as function, u64, vp
     import ctypes
     back = function("qsgd_int8_linear_backward_workspace", u64, u64, u64, u64)
     linear = function("qsgd_int8_linear_workspace", u64, vp, u64, u64, u64, u64, ctypes.c_int)
@@ -96,7 +96,7 @@ def test_bindings_refuse_host_tensors():
 def test_distill_argument_checks():
     import ctypes
 
-    from quantized_sgd_amd._ops import function, u64, vp
+    from quantized_sgd_amd._ops import bind as function, u64, vp
     from quantized_sgd_amd.distill import _Teacher, _teacher_p
     i = ctypes.c_int
     step = function("qsgd_distill_step", i, vp, i, u64, u64, u64, _teacher_p, vp, vp, vp, u64, vp, vp)
