@@ -28,6 +28,19 @@ void launch_rows(const QuantizeParams &p, hipStream_t stream) {
     else quantize_rows_kernel<T, 256, 0><<<by_group, 256, 0, stream>>>(p);
 }
 
+// Rows and the copy of a matrix in one launch.
+template <class T>
+void launch_rows_and_copy(const QuantizeParams &p, const RepackParams &w, hipStream_t stream) {
+    const uint32_t n = p.wide;
+    const uint64_t rows = n <= 1024 ? div_up(p.rows, 4) : p.rows;
+    const dim3 grid = grid_of(rows + div_up(w.rows * (w.ldd / 16), 256));
+    if (n <= 1024) layer_inputs_kernel<T, 64, 2><<<grid, 256, 0, stream>>>(p, rows, w);
+    else if (n <= 2048) layer_inputs_kernel<T, 256, 1><<<grid, 256, 0, stream>>>(p, rows, w);
+    else if (n <= 4096) layer_inputs_kernel<T, 256, 2><<<grid, 256, 0, stream>>>(p, rows, w);
+    else if (n <= 8192) layer_inputs_kernel<T, 256, 4><<<grid, 256, 0, stream>>>(p, rows, w);
+    else layer_inputs_kernel<T, 256, 0><<<grid, 256, 0, stream>>>(p, rows, w);
+}
+
 qsgd_status quantize_rows(const void *x, qsgd_dtype dtype, uint64_t rows, uint64_t cols, uint64_t ldx,
                           const float *fold, int8_t *levels, uint64_t ldl, float *scale, uint64_t wide,
                           hipStream_t stream) {
@@ -354,6 +367,19 @@ qsgd_status qsgd_int8_linear(const void *x, qsgd_dtype dtype, uint64_t ldx, cons
     if (!xq) {
         xq = (int8_t *)workspace + plan.bytes;
         sx = (float *)((char *)workspace + plan.bytes + round_up(m * ldq, 256));
+    }
+    if (n && plan.repack_b) {
+        int8_t *const copy = (int8_t *)workspace + plan.at_b;
+        const RepackParams r{w, copy, ldw, plan.ldb, (uint32_t)n, (uint32_t)k};
+        const qsgd_status st = with_type(dtype, [&](auto t) {
+            launch_rows_and_copy<decltype(t)>({x, nullptr, xq, sx, ldx, ldq, (uint32_t)m, (uint32_t)k, (uint32_t)padded16(k)}, r,
+                                              stream);
+            return launched();
+        });
+        if (st != QSGD_OK) return st;
+        Plan rest = plan;
+        rest.repack_b = false;
+        return run_matmul(rest, xq, sx, copy, sw, bias, y, dtype, ldy, ldq, plan.ldb, m, n, k, workspace, stream);
     }
     const qsgd_status st = quantize_rows(x, dtype, m, k, ldx, nullptr, xq, ldq, sx, padded16(k), stream);
     if (st != QSGD_OK || n == 0) return st;

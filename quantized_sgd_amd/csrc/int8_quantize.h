@@ -461,5 +461,14 @@ __device__ __forceinline__ void repack_block(const RepackParams &p, uint64_t blo
 
 static __global__ __launch_bounds__(256) void repack_kernel(RepackParams p) { repack_block(p, block_index()); }
 
+// The layer's rows quantized and its weight copied to aligned rows, in one launch.
+template <class T, int TPR, int NV>
+__global__ __launch_bounds__(256) void layer_inputs_kernel(QuantizeParams rows, uint64_t n_rows, RepackParams w) {
+    __shared__ uint32_t part[4];
+    const uint64_t block = block_index();
+    if (block < n_rows) quantize_rows_block<T, TPR, NV>(rows, block, part);
+    else repack_block(w, block - n_rows);
+}
+
 }  // namespace ops
 }  // namespace qsgd
