@@ -186,6 +186,8 @@ Plan plan_matmul(bool a_aligned, uint64_t lda, bool a_padded, bool b_aligned, ui
     return p;
 }
 
+uint32_t band_of(const MatmulParams &p) { return p.tiles_m <= 6 ? p.tiles_m : 4; }
+
 template <class C, class OUT>
 void launch_tiles(const MatmulParams &p, hipStream_t stream) {
     MatmulParams q = p;
@@ -193,8 +195,20 @@ void launch_tiles(const MatmulParams &p, hipStream_t stream) {
     // a tile that fills a CU: one workgroup a CU goes from tile to tile
     const bool stay = C::kLds > 80 * 1024 && tiles > kCus && p.steps_per_split >= C::S && p.splits == 1;
     q.stride = stay ? kCus / 8 : tiles;
-    q.band = p.tiles_m <= 6 ? p.tiles_m : 4;
+    q.band = band_of(p);
     matmul_kernel<C, OUT><<<dim3(stay ? (uint32_t)kCus : tiles, p.splits), C::NW * 64, 0, stream>>>(q);
+}
+
+// Two products of the same small tile, whole sums both, in one launch.
+bool pairs(const Plan &p, const Plan &q) {
+    return !p.skinny && !q.skinny && p.tile == q.tile && p.tile < 2 && p.splits == 1 && q.splits == 1;
+}
+
+template <class C, class P, class Q>
+void launch_pair(MatmulParams p, MatmulParams q, hipStream_t stream) {
+    p.band = band_of(p), q.band = band_of(q);
+    p.stride = p.tiles_m * p.tiles_n, q.stride = q.tiles_m * q.tiles_n;
+    matmul_pair_kernel<C, P, Q><<<p.stride + q.stride, C::NW * 64, 0, stream>>>(p, q, p.stride);
 }
 
 template <class OUT>
@@ -211,13 +225,18 @@ qsgd_status repack(const int8_t *src, uint64_t lds, int8_t *dst, uint64_t ldd, u
     return launched();
 }
 
+MatmulParams params_of(const Plan &plan, const int8_t *a, const float *sa, const int8_t *b, const float *sb,
+                       const float *bias, void *y, uint64_t ldy, uint64_t m, uint64_t n, uint64_t k) {
+    return {a, b, sa, sb, bias, y, nullptr, plan.lda, plan.ldb, ldy, (uint32_t)m, (uint32_t)n, (uint32_t)k,
+            (uint32_t)plan.tiles_m, (uint32_t)plan.tiles_n, (uint32_t)plan.splits, (uint32_t)plan.steps, 0, 0};
+}
+
 qsgd_status run_matmul(const Plan &plan, const int8_t *a, const float *sa, const int8_t *b, const float *sb,
                        const float *bias, void *y, qsgd_dtype dtype, uint64_t ldy, uint64_t lda, uint64_t ldb,
                        uint64_t m, uint64_t n, uint64_t k, void *workspace, hipStream_t stream) {
     if (m == 0 || n == 0) return QSGD_OK;
     char *ws = (char *)workspace;
-    MatmulParams p{a, b, sa, sb, bias, y, nullptr, plan.lda, plan.ldb, ldy, (uint32_t)m, (uint32_t)n, (uint32_t)k,
-                   (uint32_t)plan.tiles_m, (uint32_t)plan.tiles_n, (uint32_t)plan.splits, (uint32_t)plan.steps};
+    MatmulParams p = params_of(plan, a, sa, b, sb, bias, y, ldy, m, n, k);
     if (plan.repack_a) {
         p.a = (const int8_t *)(ws + plan.at_a);
         const qsgd_status st = repack(a, lda, (int8_t *)(ws + plan.at_a), plan.lda, m, k, stream);
@@ -423,6 +442,16 @@ qsgd_status qsgd_int8_linear_backward(const void *gy, qsgd_dtype dtype, uint64_t
         if (columns) launch_transpose<T>(p.columns, stream);
         return launched();
     });
+    if (st == QSGD_OK && rows && columns && pairs(b.gx, b.gw)) {
+        const MatmulParams x = params_of(b.gx, gq, sg, wt, nullptr, nullptr, gx, ldgx, m, k, n);
+        const MatmulParams y = params_of(b.gw, hq, sh, xt, nullptr, nullptr, gw, ldgw, n, k, m);
+        return with_type(dtype, [&](auto t) {
+            using T = decltype(t);
+            if (b.gx.tile == 0) launch_pair<Tile64, T, float>(x, y, stream);
+            else launch_pair<Tile128, T, float>(x, y, stream);
+            return launched();
+        });
+    }
     if (st == QSGD_OK && gx)
         st = run_matmul(b.gx, gq, sg, wt, nullptr, nullptr, gx, dtype, ldgx, b.ldn, b.ldn, m, k, n, ws + b.own, stream);
     if (st == QSGD_OK && gw)

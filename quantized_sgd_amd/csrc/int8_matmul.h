@@ -119,9 +119,9 @@ struct no {
     static constexpr bool value = false;
 };
 
+// `block`: the workgroup's place among those of the product; `part`: of the sum.
 template <class C, class OUT>
-__global__ __launch_bounds__(C::NW * 64, 1) void matmul_kernel(MatmulParams p) {
-    __shared__ __align__(1024) int8_t ring[C::kLds];
+__device__ __forceinline__ void matmul_block(const MatmulParams &p, int8_t *ring, const uint32_t block, const uint32_t part) {
     const uint32_t lane = threadIdx.x & 63;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t wm = wave / C::WN, wn = wave % C::WN;
@@ -130,12 +130,12 @@ __global__ __launch_bounds__(C::NW * 64, 1) void matmul_kernel(MatmulParams p) {
     // tiles, in bands of tile rows, so that the tiles an XCD works on together
     // share their rows of a and b in its L2 (8192^3: bands of 4 422 us, 2 431, 6 428, 8 436).
     const uint32_t tiles = p.tiles_m * p.tiles_n;
-    const uint32_t xcd = blockIdx.x % 8;
+    const uint32_t xcd = block % 8;
     const uint32_t run = tiles / 8 + (xcd < tiles % 8), first = xcd * (tiles / 8) + min(xcd, tiles % 8);
-    uint32_t nth = blockIdx.x / 8;
+    uint32_t nth = block / 8;
     if (nth >= run) return;
 
-    const uint32_t k0 = blockIdx.y * p.steps_per_split;  // first step
+    const uint32_t k0 = part * p.steps_per_split;  // first step
     const uint32_t all = (p.k + 127) / 128;
     const uint32_t steps = min(p.steps_per_split, all - k0);
     const uint32_t full = min(steps, p.k / 128 - min(p.k / 128, k0));  // steps wholly inside k
@@ -186,8 +186,8 @@ __global__ __launch_bounds__(C::NW * 64, 1) void matmul_kernel(MatmulParams p) {
     const auto fill = [&](auto fast, int j, uint32_t step, uint32_t slot) __attribute__((always_inline)) {
         const bool of_a = j < C::LA;
         const int q = of_a ? j : j - C::LA;
-        const uint32_t part = wave * (of_a ? C::LA : C::LB) + q;
-        const uint32_t to = lds0 + slot * C::kStage + (of_a ? 0 : C::BM * 128) + part * 1024;
+        const uint32_t nth_load = wave * (of_a ? C::LA : C::LB) + q;
+        const uint32_t to = lds0 + slot * C::kStage + (of_a ? 0 : C::BM * 128) + nth_load * 1024;
         const int8_t *from = (of_a ? a : b) + (uint64_t)step * 128;
         const uint32_t offset = of_a ? oa[q] : ob[q];
         if (decltype(fast)::value) {
@@ -195,7 +195,7 @@ __global__ __launch_bounds__(C::NW * 64, 1) void matmul_kernel(MatmulParams p) {
         } else {
             // the step that the end of k cuts, and the ring's steps past it: zeros
             const uint32_t inside = step < full ? 128u : step < steps ? p.k % 128 : 0u;
-            load_to_lds(to, (part & 1 ? chunk1 : chunk0) < inside ? from + offset : (const int8_t *)kZeros);
+            load_to_lds(to, (nth_load & 1 ? chunk1 : chunk0) < inside ? from + offset : (const int8_t *)kZeros);
         }
     };
 
@@ -363,7 +363,7 @@ __global__ __launch_bounds__(C::NW * 64, 1) void matmul_kernel(MatmulParams p) {
                 for (int f = 0; f < C::TN; ++f) {
                     const uint32_t n0 = bn + (wn * C::TN + f) * 16 + (lane >> 4) * 4;
                     if (n0 >= p.n) continue;
-                    int32_t *out = p.part + ((uint64_t)blockIdx.y * p.m + m0 + j * 16) * p.n + n0;
+                    int32_t *out = p.part + ((uint64_t)part * p.m + m0 + j * 16) * p.n + n0;
                     if (n0 + 4 <= p.n) __builtin_memcpy(out, &acc[f][j], 16);
                     else
                         for (int e = 0; e < 4; ++e)
@@ -377,6 +377,22 @@ __global__ __launch_bounds__(C::NW * 64, 1) void matmul_kernel(MatmulParams p) {
         if (!more) break;
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load may land after the workgroup's end
+}
+
+template <class C, class OUT>
+__global__ __launch_bounds__(C::NW * 64, 1) void matmul_kernel(MatmulParams p) {
+    __shared__ __align__(1024) int8_t ring[C::kLds];
+    matmul_block<C, OUT>(p, ring, blockIdx.x, blockIdx.y);
+}
+
+// Two products that do not need each other, the first `blocks` workgroups on p: alone
+// neither fills the chip's last round of workgroups (the gradient of 1000 x 777 x 1537:
+// 27 us, 32 with a launch each; of 2048 x 2048 x 1536: 43 and 55).
+template <class C, class P, class Q>
+__global__ __launch_bounds__(C::NW * 64, 1) void matmul_pair_kernel(MatmulParams p, MatmulParams q, uint32_t blocks) {
+    __shared__ __align__(1024) int8_t ring[C::kLds];
+    if (blockIdx.x < blocks) matmul_block<C, P>(p, ring, blockIdx.x, 0);
+    else matmul_block<C, Q>(q, ring, blockIdx.x - blocks, 0);
 }
 
 // Joins the parts of a split sum: exact in 64 bits, then the epilogue.

@@ -71,7 +71,7 @@ def _teacher(z, idx, t, tau, teacher_lse):
 
 def _gradient_out(z, ldz, out):
     if out is None:
-        return torch.empty(z.shape, dtype=z.dtype, device=z.device), max(z.shape[1], 1)
+        return torch.empty(*z.shape, dtype=z.dtype, device=z.device), max(z.shape[1], 1)
     ld = matrix(out, "out", (z.dtype,), *z.shape, z.device)
     if out.data_ptr() == z.data_ptr() and ld != ldz:
         raise ValueError("out in z's place must have z's row stride")
@@ -91,7 +91,7 @@ def distill_topk(z: torch.Tensor, idx: torch.Tensor, t: torch.Tensor, tau: float
     dev = z.device
     with on(dev, stream):
         loss = torch.empty(rows, dtype=torch.float32, device=dev)
-        stats = torch.empty((rows, 4), dtype=torch.float32, device=dev)
+        stats = torch.empty(rows, 4, dtype=torch.float32, device=dev)
         ws = scratch(_workspace_bytes(rows, vocab, DTYPE[z.dtype]), dev)
         check(_c("qsgd_distill_forward")(
             z.data_ptr(), DTYPE[z.dtype], rows, vocab, ldz, te, loss.data_ptr(), stats.data_ptr(),

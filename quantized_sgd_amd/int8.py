@@ -73,7 +73,7 @@ def int8_quantize(x: torch.Tensor, fold=None, transpose: bool = False, out=None,
     f = vector(fold, "fold", length, dev)
     with on(dev, stream):
         if out is None:
-            out, ldl = torch.empty((n, length), dtype=torch.int8, device=dev), max(length, 1)
+            out, ldl = torch.empty(n, length, dtype=torch.int8, device=dev), max(length, 1)
         else:
             ldl = matrix(out, "out", _I8, n, length, dev)
         if scale is None:
@@ -106,7 +106,7 @@ def int8_matmul(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb=None, bia
     pa, pb, pbias = vector(sa, "sa", m, dev), vector(sb, "sb", n, dev), vector(bias, "bias", n, dev)
     with on(dev, stream):
         if out is None and dtype in FLOATS:
-            out, ldy = torch.empty((m, n), dtype=dtype, device=dev), max(n, 1)
+            out, ldy = torch.empty(m, n, dtype=dtype, device=dev), max(n, 1)
         elif out is None:
             raise ValueError(f"dtype must be one of {', '.join(map(str, FLOATS))}, got {dtype}")
         else:
@@ -134,7 +134,7 @@ def int8_linear(x: torch.Tensor, w: torch.Tensor, sw: torch.Tensor, bias=None, k
     psw, pbias = vector(sw, "sw", n, dev), vector(bias, "bias", n, dev)
     with on(dev, stream):
         if out is None:
-            out, ldy = torch.empty((m, n), dtype=x.dtype, device=dev), max(n, 1)
+            out, ldy = torch.empty(m, n, dtype=x.dtype, device=dev), max(n, 1)
         else:
             ldy = matrix(out, "out", (x.dtype,), m, n, dev)
         wp = w.data_ptr()
