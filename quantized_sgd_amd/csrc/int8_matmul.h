@@ -101,7 +101,10 @@ __device__ __forceinline__ void multiply_add(v4i &acc, const v4i &b, const v4i &
 }
 __device__ __forceinline__ void settle() { asm volatile("s_nop 15\n\ts_nop 7" ::: "memory"); }
 __device__ __forceinline__ void start() { asm volatile("s_nop 3"); }  // between writing accumulators and a product
-__device__ __forceinline__ void settled(v4i &acc) { asm volatile("" : "+a"(acc)); }
+// An accumulator's value, moved out of its registers here and not before: moved ahead
+// of the epilogue's branches by the compiler, the values of a large tile did not fit
+// the other registers and went through memory (8192^3 into fp32 524 us, 412 without).
+__device__ __forceinline__ v4i settled(v4i acc) { asm volatile("" : "+v"(acc)); return acc; }
 
 // The column of y, within 32, that row i of b's fragment f (of a pair) belongs to.
 // A lane's accumulators of a pair are rows 4 g to 4 g + 3 of both (g = lane / 16), and
@@ -310,10 +313,6 @@ __device__ __forceinline__ void matmul_block(const MatmulParams &p, int8_t *ring
             half(no{}, yes{}, later);
         }
         settle();
-#pragma unroll
-        for (int i = 0; i < C::TN; ++i)
-#pragma unroll
-            for (int j = 0; j < C::TM; ++j) settled(acc[i][j]);
 
         // Epilogue: kCols columns of a lane at a time (16 bytes of y). A tile wholly
         // inside y goes without tests between its stores.
@@ -343,10 +342,13 @@ __device__ __forceinline__ void matmul_block(const MatmulParams &p, int8_t *ring
 #pragma unroll
                 for (int j = 0; j < C::TM; ++j, out += down) {
                     if (!kInside && m0 + j * 16 >= p.m) continue;
+                    v4i sum[kFrags];
                     OUT v[kCols];
 #pragma unroll
+                    for (int e = 0; e < kFrags; ++e) sum[e] = settled(acc[f + e][j]);
+#pragma unroll
                     for (int e = 0; e < kCols; ++e)
-                        v[e] = (OUT)((float)acc[f + e / 4][j][e % 4] * sa[j] * sb[e] + bias[e]);
+                        v[e] = (OUT)((float)sum[e / 4][e % 4] * sa[j] * sb[e] + bias[e]);
                     if (there == kCols) __builtin_memcpy(out, v, sizeof(v));
                     else
 #pragma unroll
@@ -363,11 +365,12 @@ __device__ __forceinline__ void matmul_block(const MatmulParams &p, int8_t *ring
                 for (int f = 0; f < C::TN; ++f) {
                     const uint32_t n0 = bn + (wn * C::TN + f) * 16 + (lane >> 4) * 4;
                     if (n0 >= p.n) continue;
+                    const v4i sum = settled(acc[f][j]);
                     int32_t *out = p.part + ((uint64_t)part * p.m + m0 + j * 16) * p.n + n0;
-                    if (n0 + 4 <= p.n) __builtin_memcpy(out, &acc[f][j], 16);
+                    if (n0 + 4 <= p.n) __builtin_memcpy(out, &sum, 16);
                     else
                         for (int e = 0; e < 4; ++e)
-                            if (n0 + e < p.n) out[e] = acc[f][j][e];
+                            if (n0 + e < p.n) out[e] = sum[e];
                 }
             }
         };
