@@ -137,10 +137,18 @@ struct Entries {
     float red[2 * 16];
 };
 
+// log(1 - x), to the last places of a small x: log(w) of the rounded w = 1 - x, times
+// x / (1 - w), which undoes the rounding (W. Kahan's method).
+__device__ __forceinline__ float log_rest_of(float x) {
+    const float w = 1.0f - x;
+    return w == 1.0f ? -x : logf(w) * (x / (1.0f - w));
+}
+
 struct TeacherSums {
     bool some;      // the row has an entry
     float shift;    // log p = t / tau - shift
     float rest;     // p_r
+    float log_rest; // log p_r
 };
 
 // Reads a row's entries (by the whole workgroup; ends with a barrier). `ahead` is
@@ -170,6 +178,7 @@ __device__ __forceinline__ TeacherSums read_entries(const DistillParams &p, uint
             sum += v;
         }
         sum = block_sum(sum, e.red);
+        s.log_rest = log_rest_of(sum);
         s.rest = sum >= 1.0f ? 0.0f : 1.0f - sum;  // NaN stays
     } else {
         top = base_of(block_max(top, e.red));
@@ -182,7 +191,7 @@ __device__ __forceinline__ TeacherSums read_entries(const DistillParams &p, uint
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
         for (uint32_t i = threadIdx.x; i < p.k; i += blockDim.x) e.p[i] *= inv;
         s.shift = top + logf(sum);
-        s.rest = 0.0f;
+        s.rest = s.log_rest = 0.0f;
     }
     __syncthreads();
     return s;
@@ -243,10 +252,19 @@ struct Stats {
 
 __device__ __forceinline__ float inverse(float s) { return s == 0.0f ? 0.0f : 1.0f / s; }
 
-// The remainder's term of the loss.
-__device__ __forceinline__ float rest_loss(const DistillParams &p, const TeacherSums &ts, Pair rest, float base, float log_sum) {
-    if (!p.teacher_lse || ts.rest == 0.0f || rest.s == 0.0f) return 0.0f;
-    return ts.rest * (logf(ts.rest) - ((base_of(rest.m) - base) * p.inv_tau + logf(rest.s) - log_sum));
+// The remainder's term of the loss, p_r (log p_r - log q_r), with the probability
+// `inside` that the student gives the entries. Where the entries hold little, both
+// logarithms are close to 0 and the term cancels against the entries' terms (a flat
+// distribution's few entries make a loss of 1e-4 out of terms of 1e-2), so they are
+// taken from what the entries hold and not from sums over the rest: 3 entries of 30912
+// at tau 4 come out 1e-6 off, 2e-3 the other way. `inside` has to be the sum of the
+// exponentials of the very log q that the entries' terms use: an error of those then
+// moves both sides alike.
+__device__ __forceinline__ float rest_loss(const DistillParams &p, const TeacherSums &ts, Pair rest, float base, float log_sum,
+                                           float inside) {
+    if (ts.rest == 0.0f || rest.s == 0.0f) return 0.0f;
+    const float log_q = inside < 0.5f ? log_rest_of(inside) : (base_of(rest.m) - base) * p.inv_tau + logf(rest.s) - log_sum;
+    return ts.rest * (ts.log_rest - log_q);
 }
 
 __device__ __forceinline__ Stats finish_row(const DistillParams &p, uint32_t row, const TeacherSums &ts, Pair scanned,
@@ -259,16 +277,17 @@ __device__ __forceinline__ Stats finish_row(const DistillParams &p, uint32_t row
         all = join(all, block_join(top, c, e.red), c);
     }
     const float log_sum = logf(all.s), base = base_of(all.m);
-    float loss = 0.0f;
+    float loss = 0.0f, inside = 0.0f;
     for (uint32_t i = threadIdx.x; i < p.k; i += blockDim.x) {
         const float pi = e.p[i];
-        if (e.at[i] < 0 || pi == 0.0f) continue;
+        if (e.at[i] < 0) continue;
         const float log_p = e.t[i] - ts.shift;
         const float log_q = all.s == 0.0f ? -INFINITY : (e.z[i] - base) * p.inv_tau - log_sum;
-        loss += pi * (log_p - log_q);
+        if (p.teacher_lse) inside += expf(log_q);
+        if (pi != 0.0f) loss += pi * (log_p - log_q);
     }
     loss = block_sum(loss, e.red);
-    loss += rest_loss(p, ts, scanned, base, log_sum);
+    if (p.teacher_lse) loss += rest_loss(p, ts, scanned, base, log_sum, block_sum(inside, e.red));
     if (threadIdx.x == 0 && p.loss) p.loss[row] = ts.some ? loss : 0.0f;
     return {all.m, inverse(all.s), scanned.m, inverse(scanned.s)};
 }
@@ -408,12 +427,13 @@ __global__ __launch_bounds__(THREADS) void distill_resident_kernel(DistillParams
     if (tail) {
         const float sum = wave_sum(in ? red[1][lane] : 0.0f);
         ts.shift = lse;
+        ts.log_rest = log_rest_of(sum);
         ts.rest = sum >= 1.0f ? 0.0f : 1.0f - sum;  // NaN stays
         if (marks && at >= 0) atomicOr(&bits[at / 32], 1u << (at % 32));
     } else {
         te = wave_join({in ? red[0][lane] : -INFINITY, in ? red[1][lane] : 0.0f}, kLog2e);
         ts.shift = base_of(te.m) + logf(te.s);
-        ts.rest = 0.0f;
+        ts.rest = ts.log_rest = 0.0f;
         prob = at >= 0 ? exp_scaled(t, base_of(te.m), kLog2e) * inverse(te.s) : 0.0f;
     }
     __syncthreads();
@@ -463,15 +483,19 @@ __global__ __launch_bounds__(THREADS) void distill_resident_kernel(DistillParams
 
         // loss
         const float log_sum = logf(all.s), base = base_of(all.m), zt = at >= 0 ? (float)zt_raw : -INFINITY;
-        float loss = 0.0f;
-        if (at >= 0 && prob != 0.0f)
-            loss = prob * (t - ts.shift - (all.s == 0.0f ? -INFINITY : (zt - base) * p.inv_tau - log_sum));
+        const float log_q = all.s == 0.0f ? -INFINITY : (zt - base) * p.inv_tau - log_sum;
+        float loss = at >= 0 && prob != 0.0f ? prob * (t - ts.shift - log_q) : 0.0f, inside = 0.0f;
         loss = wave_sum(loss);
+        if (tail) inside = wave_sum(at >= 0 ? expf(log_q) : 0.0f);
         __syncthreads();
-        if (lane == 0) red[0][wave] = loss;
+        if (lane == 0) {
+            red[0][wave] = loss;
+            red[1][wave] = inside;
+        }
         __syncthreads();
         if (wave == 0) {
-            loss = wave_sum(in ? red[0][lane] : 0.0f) + rest_loss(p, ts, v, base, log_sum);
+            loss = wave_sum(in ? red[0][lane] : 0.0f);
+            if (tail) loss += rest_loss(p, ts, v, base, log_sum, wave_sum(in ? red[1][lane] : 0.0f));
             if (lane == 0) p.loss[row] = ts.some ? loss : 0.0f;
         }
     }
