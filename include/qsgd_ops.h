@@ -61,7 +61,7 @@ qsgd_status qsgd_int8_quantize_transposed(const void *x, qsgd_dtype dtype, uint6
 
 /*
  * qsgd_int8_matmul: y[i, j] = RN(RN32(RN32(RN32(acc) sa[i]) sb[j]) + bias[j]) with
- * acc = sum_p a[i, p] b[j, p], exact for every k below 2^31.
+ * acc = sum_p a[i, p] b[j, p], exact. k is at most 2^23 (else QSGD_ERR_UNSUPPORTED).
  *   a     [m, k] int8, row stride lda; sa [m] fp32 (a token's scale).
  *   b     [n, k] int8, row stride ldb; sb [n] fp32 (a channel's scale) or NULL (1).
  *   bias  [n] fp32 or NULL.
@@ -78,7 +78,8 @@ qsgd_status qsgd_int8_matmul(const int8_t *a, uint64_t lda, const float *sa, con
 
 /*
  * qsgd_int8_linear: the layer. Quantizes the rows of x and multiplies:
- * y = qsgd_int8_matmul(levels and scale of x, w, sw, bias), in x's type.
+ * y = qsgd_int8_matmul(levels and scale of x, w, sw, bias), in x's type. k is at most
+ * 2^23 (else QSGD_ERR_UNSUPPORTED).
  *   x   [m, k] of `dtype`, row stride ldx.
  *   w   [n, k] int8 levels of the weight, row stride ldw; sw [n] fp32.
  *   xq  [m, ldxq] int8 and sx [m] fp32 outputs: the levels (columns past k up to
@@ -103,7 +104,8 @@ qsgd_status qsgd_int8_linear(const void *x, qsgd_dtype dtype, uint64_t ldx, cons
  *   gq, sg = rows of gy quantized with fold = sw;     gx[i, p] = RN(sg[i] sum_j gq[i, j] w[j, p])
  *   hq, sh = columns of gy quantized with fold = sx;  gw[j, p] = RN32(sh[j] sum_i hq[i, j] xq[i, p])
  * Each entry of gx is within sum_j |w[j, p]| sg[i] / 2 of the product in reals
- * (up to fp32 rounding), and of gw within sum_i |xq[i, p]| sh[j] / 2.
+ * (up to fp32 rounding), and of gw within sum_i |xq[i, p]| sh[j] / 2. m and n are at
+ * most 2^23 (else QSGD_ERR_UNSUPPORTED).
  *   gy  [m, n] of `dtype`, row stride ldgy.
  *   xq  [m, k] int8, row stride ldxq, sx [m], w [n, k], sw [n]: as in the layer.
  *   gx  [m, k] of `dtype`, row stride ldgx, or NULL (not computed).

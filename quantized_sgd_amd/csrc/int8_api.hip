@@ -13,8 +13,9 @@ namespace {
 
 // ---- quantizer ----
 
-// Rows of up to 2048 values are a wave's, longer ones a workgroup's; beyond 16384
-// they are read twice.
+// Rows of up to 1024 values are a wave's, longer ones a workgroup's, with as many
+// registers as they need (16384 rows of 1024 values: 11.1 us, 17.5 by workgroups);
+// beyond 16384 values they are read twice.
 template <class T>
 void launch_rows(const QuantizeParams &p, hipStream_t stream) {
     const dim3 by_wave = grid_of(div_up(p.rows, 4)), by_group = grid_of(p.rows);
@@ -53,11 +54,12 @@ qsgd_status quantize_rows(const void *x, qsgd_dtype dtype, uint64_t rows, uint64
 }
 
 // Runs of rows for the column maxima, of at least 32 rows: few enough to be joined
-// where they are used for up to 2048 rows (it saves a launch), else enough
-// workgroups for the chip.
+// where they are used for up to 1024 rows (it saves a launch), else enough
+// workgroups for the chip (1021 x 5003: 17.2 us with few, 17.0 with many; 2048 x 4096:
+// 19.4 and 16.9; 8192 x 4096: 56 and 37).
 uint32_t column_splits(uint64_t rows, uint64_t cols) {
     const uint64_t blocks = std::max<uint64_t>(1, div_up(cols, 512));
-    const uint64_t most = rows <= 2048 ? kFewSplits : std::min<uint64_t>(kMaxSplits, div_up(1024, blocks));
+    const uint64_t most = rows <= 1024 ? kFewSplits : std::min<uint64_t>(kMaxSplits, div_up(1024, blocks));
     return (uint32_t)std::max<uint64_t>(1, std::min(most, div_up(rows, 32)));
 }
 
@@ -186,13 +188,17 @@ Plan plan_matmul(bool a_aligned, uint64_t lda, bool a_padded, bool b_aligned, ui
     return p;
 }
 
+// Tile rows gone through together: four share what an XCD's L2 holds; with few rows
+// all of them, so that a column of b is read once (515 x 4099 x 2064, five rows of 128:
+// 16.8 us, 18.6 in bands of four).
 uint32_t band_of(const MatmulParams &p) { return p.tiles_m <= 6 ? p.tiles_m : 4; }
 
 template <class C, class OUT>
 void launch_tiles(const MatmulParams &p, hipStream_t stream) {
     MatmulParams q = p;
     const uint32_t tiles = p.tiles_m * p.tiles_n;
-    // a tile that fills a CU: one workgroup a CU goes from tile to tile
+    // a tile that fills a CU: one workgroup a CU goes from tile to tile (8192^3: 494 us,
+    // 511 with a workgroup a tile, when this was built)
     const bool stay = C::kLds > 80 * 1024 && tiles > kCus && p.steps_per_split >= C::S && p.splits == 1;
     q.stride = stay ? kCus / 8 : tiles;
     q.band = band_of(p);
