@@ -24,7 +24,6 @@ namespace ops {
 constexpr int kMaxEntries = 1024;
 constexpr uint32_t kMaxSegment = 1u << 18;  // logits of a workgroup: 32 KB of bits
 constexpr int kDT = 512;                    // threads of a workgroup
-constexpr int kDW = kDT / 64;
 
 struct DistillParams {
     const void *z, *idx, *t;
